@@ -358,6 +358,69 @@ W4A16_API int w4a16_gemm_noalloc(const void* A, int a_dtype, int M, int K, const
                                  void* C, void* stream);
 
 /*
+ * Routed layers: the rows of one batch each pick, beside the INT4 format they share, a matrix of
+ * their own (an expert of a mixture). The pages treat one weight for all rows; these entry points
+ * are this library's own. A run of them:
+ *   w4a16_moe_sort (tokens -> sorted rows), the experts' layers on the sorted rows,
+ *   w4a16_moe_combine (sorted rows -> tokens); w4a16_moe_combine_grad and w4a16_moe_sort_grad back.
+ *
+ * A router gives token t (t < T) the experts ids[t, j], j < k. With the flat index i = t k + j,
+ *   slots[i]  = number of ids below ids[i], plus the number of equal ones before i: the sorted row
+ *               of choice i (a stable sort by expert); -1 where ids[i] is outside [0, E), a choice
+ *               without a row (a padded or dropped one),
+ *   rows[s]   = the flat index i whose sorted row is s,
+ *   offsets[e] = first sorted row of expert e, offsets[E] = rows in all (<= T k).
+ * One token may name one expert twice: those are two rows. Sorted rows at or past offsets[E] are
+ * neither read nor written by any of these entry points: buffers keep what they held there.
+ * Shapes: T >= 1, 1 <= k <= 32, 1 <= E <= 1024, T k <= 2^30, H >= 8, H % 8 == 0.
+ *
+ * w4a16_moe_sort -- the sort and the gather of the rows, Xs[slots[t, j]] = X[t] (copied bits).
+ * Arguments
+ *   ids        device, int32 [T, k].
+ *   T, k, E    tokens, choices per token, experts.
+ *   X          device, 16-bit [T, H] row-major, or NULL for the maps alone (then H is ignored and
+ *              Xs must be NULL).
+ *   H          row length.
+ *   offsets    device out, int32 [E + 1].
+ *   rows       device out, int32 [T k] (entries at or past offsets[E] are left as they were).
+ *   slots      device out, int32 [T, k].
+ *   Xs         device out, 16-bit [T k, H]. Must not overlap X.
+ *   workspace, ws_bytes   device, at least w4a16_moe_sort_workspace_bytes(T, k, E) bytes, 16-byte
+ *              aligned (NULL when that is 0); contents on entry do not matter. Calls that share
+ *              one must be ordered on the GPU.
+ *   stream     cudaStream_t. One kernel launch, two above 8192 ids.
+ *
+ * w4a16_moe_sort_grad -- the gather's gradient: dX[t] = sum_j dXs[slots[t, j]], FP32 sums in the order
+ *   of j, rounded once; choices without a row add nothing (a token without any gets 0).
+ *   dXs device [T k, H] of dtype, slots device int32 [T, k], dX device out [T, H] of dtype.
+ *
+ * w4a16_moe_combine -- Y[t] = sum_j weights[t, j] Ys[slots[t, j]], FP32, rounded once; choices
+ *   without a row add nothing, whatever their weight.
+ *   Ys device [T k, H] of dtype, weights device fp32 [T, k] or NULL (all 1), Y device out [T, H].
+ *
+ * w4a16_moe_combine_grad -- the gradient of w4a16_moe_combine: dYs[slots[t, j]] = weights[t, j] dY[t]
+ *   (rounded once; rows at or past offsets[E] untouched), dweights[t, j] = sum_h dY[t, h]
+ *   Ys[slots[t, j], h] in FP32 (0 for a choice without a row). The sums' order is fixed: results do
+ *   not change from run to run.
+ *   dY device [T, H], Ys device [T k, H] (may be NULL when dweights is), dYs device out [T k, H],
+ *   dweights device out fp32 [T, k] or NULL.
+ * A slot outside [0, T k) counts as a choice without a row; slots of one call are distinct, as
+ * w4a16_moe_sort writes them. dtype: W4A16_F16 or W4A16_BF16. No buffer may overlap an output.
+ * Return W4A16_OK, W4A16_EINVAL, W4A16_EALIGN, W4A16_EWORKSPACE or W4A16_ECUDA.
+ */
+W4A16_API size_t w4a16_moe_sort_workspace_bytes(int T, int k, int E);
+W4A16_API int w4a16_moe_sort(const int32_t* ids, int T, int k, int E, const void* X, int H, int32_t* offsets,
+                             int32_t* rows, int32_t* slots, void* Xs, void* workspace, size_t ws_bytes,
+                             void* stream);
+W4A16_API int w4a16_moe_sort_grad(const void* dXs, int dtype, int T, int k, int H, const int32_t* slots, void* dX,
+                                  void* stream);
+W4A16_API int w4a16_moe_combine(const void* Ys, int dtype, int T, int k, int H, const int32_t* slots,
+                                const float* weights, void* Y, void* stream);
+W4A16_API int w4a16_moe_combine_grad(const void* dY, const void* Ys, int dtype, int T, int k, int H,
+                                     const int32_t* slots, const float* weights, void* dYs, float* dweights,
+                                     void* stream);
+
+/*
  * w4a16_set_wait_limit_ns -- the time limit of every bounded wait inside the library's kernels
  *   (a pipeline barrier, or a counter another CTA of the same launch sets), in nanoseconds, for
  *   launches made after the call; 0 restores the default of 2 s. Returns the previous limit.

@@ -1,0 +1,50 @@
+"""Oracle of the routed layers, in numpy and FP64, from the definitions in include/w4a16.h.
+
+TEST INFRASTRUCTURE ONLY: shares no code with the CUDA library. 16-bit values come in and go out
+as float64 (the caller widens and rounds), maps as integers.
+"""
+import numpy as np
+
+
+def sort(ids, E):
+    """(offsets [E + 1], rows [R], slots [T, k]) of ids [T, k]: choice by choice, expert by expert."""
+    flat = np.asarray(ids).reshape(-1)
+    slots = np.full(flat.size, -1, dtype=np.int64)
+    offsets = np.zeros(E + 1, dtype=np.int64)
+    rows = []
+    for e in range(E):
+        offsets[e] = len(rows)
+        for i in np.flatnonzero(flat == e):
+            slots[i] = len(rows)
+            rows.append(i)
+    offsets[E] = len(rows)
+    return offsets, np.asarray(rows, dtype=np.int64), slots.reshape(np.asarray(ids).shape)
+
+
+def combine(Ys, slots, weights):
+    """(Y [T, H], sum of the magnitudes of its terms)."""
+    T, k = slots.shape
+    Y = np.zeros((T, Ys.shape[1]))
+    Yabs = np.zeros_like(Y)
+    for t in range(T):
+        for j in range(k):
+            if 0 <= slots[t, j] < T * k:
+                w = 1.0 if weights is None else float(weights[t, j])
+                term = w * Ys[slots[t, j]]
+                Y[t] += term
+                Yabs[t] += np.abs(term)
+    return Y, Yabs
+
+
+def combine_grad(dY, Ys, slots, weights):
+    """(dYs {row: values}, dweights [T, k], sum of the magnitudes of each weight's terms)."""
+    T, k = slots.shape
+    dYs, dw, dwabs = {}, np.zeros((T, k)), np.zeros((T, k))
+    for t in range(T):
+        for j in range(k):
+            s = int(slots[t, j])
+            if 0 <= s < T * k:
+                dYs[s] = (1.0 if weights is None else float(weights[t, j])) * dY[t]
+                dw[t, j] = dY[t] @ Ys[s]
+                dwabs[t, j] = np.abs(dY[t]) @ np.abs(Ys[s])
+    return dYs, dw, dwabs

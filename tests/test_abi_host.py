@@ -300,3 +300,59 @@ def test_log_environment_prints_the_dispatch(L):
     assert "[w4a16] gemm M=1 N=256 K=256 g=128 sym=0 layout=1 -> gemv" in r.stderr
     r = _in_child({"W4A16_LOG": "0", "CUDA_VISIBLE_DEVICES": ""}, code)
     assert "[w4a16]" not in r.stderr
+
+
+def test_moe_route_rejects_bad_arguments_before_any_launch(L):
+    P = ctypes.c_void_p
+    p = [P((i + 1) << 20) for i in range(8)]
+    mis = P((9 << 20) + 8)
+    assert L.w4a16_moe_sort_workspace_bytes(16, 4, 64) == 0              # up to 8192 ids
+    assert L.w4a16_moe_sort_workspace_bytes(2048, 8, 64) == 8 * 64 * 4   # a histogram per 2048 ids
+    assert L.w4a16_moe_sort_workspace_bytes(0, 4, 64) == 0
+
+    def sort(ids=p[0], T=4, k=2, E=8, X=p[1], H=64, off=p[2], rows=p[3], slots=p[4], Xs=p[5], ws=None, wsb=0):
+        return L.w4a16_moe_sort(ids, T, k, E, X, H, off, rows, slots, Xs, ws, wsb, None)
+    assert sort(T=0) == native.EINVAL
+    assert sort(k=0) == native.EINVAL
+    assert sort(k=33) == native.EINVAL
+    assert sort(E=0) == native.EINVAL
+    assert sort(E=1025) == native.EINVAL
+    assert sort(T=1 << 30) == native.EINVAL                              # T k > 2^30
+    assert sort(ids=None) == native.EINVAL
+    assert sort(off=None) == native.EINVAL
+    assert sort(slots=None) == native.EINVAL
+    assert sort(X=None) == native.EINVAL                                 # Xs without X
+    assert sort(Xs=None) == native.EINVAL
+    assert sort(H=60) == native.EINVAL
+    assert sort(X=mis) == native.EALIGN
+    assert sort(T=8192) == native.EWORKSPACE
+    assert sort(T=8192, ws=mis, wsb=1 << 20) == native.EALIGN
+
+    def comb(Ys=p[0], dt=0, T=4, k=2, H=64, slots=p[1], w=p[2], Y=p[3]):
+        return L.w4a16_moe_combine(Ys, dt, T, k, H, slots, w, Y, None)
+    assert comb(dt=2) == native.EINVAL
+    assert comb(H=4) == native.EINVAL
+    assert comb(T=-1) == native.EINVAL
+    assert comb(slots=None) == native.EINVAL
+    assert comb(w=mis) == native.EALIGN
+    assert L.w4a16_moe_sort_grad(p[0], 0, 4, 2, 60, p[1], p[3], None) == native.EINVAL
+
+    def grad(dY=p[0], Ys=p[1], dt=0, T=4, k=2, H=64, slots=p[2], w=p[3], dYs=p[4], dw=p[5]):
+        return L.w4a16_moe_combine_grad(dY, Ys, dt, T, k, H, slots, w, dYs, dw, None)
+    assert grad(Ys=None) == native.EINVAL                                # dweights needs Ys
+    assert grad(dYs=None) == native.EINVAL
+    assert grad(k=40) == native.EINVAL
+    assert grad(dY=mis) == native.EALIGN
+
+
+def test_routed_binding_refuses_what_does_not_fit():
+    """Wrong device, type, shape or stride: an error before any call into the library."""
+    import torch
+
+    ids = torch.zeros(4, 2, dtype=torch.int32)
+    for call in (lambda: native.w4a16_moe_sort(ids, 8),
+                 lambda: native.w4a16_moe_combine(torch.zeros(8, 16, dtype=torch.float16), ids),
+                 lambda: native.w4a16_moe_combine_grad(torch.zeros(4, 16, dtype=torch.float16), None, ids)):
+        with pytest.raises(native.W4A16Error) as e:
+            call()
+        assert e.value.status == native.EINVAL

@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "common.cuh"
+#include "routed.cuh"
 #include "tiled_layout.cuh"
 
 using namespace w4a16;
@@ -304,6 +305,75 @@ W4A16_API int w4a16_gemm(const void* A, int a_dtype, int M, int K, const void* w
         return launch_gemm_tc(A, a_dtype, M, K, wq, N, group, sym, C, workspace, dev_status, s);
     }
     return W4A16_EUNSUPPORTED;
+}
+
+// ------------------------------------------------------------------------------ routed layers
+static int check_route(int T, int k, int E) {
+    if (T < 1 || k < 1 || k > kRouteMaxChoices || E < 1 || E > kRouteMaxBins) return W4A16_EINVAL;
+    return (long long)T * k <= (1ll << 30) ? W4A16_OK : W4A16_EINVAL;
+}
+
+static int check_route_rows(int dtype, int H) {
+    if (dtype != W4A16_F16 && dtype != W4A16_BF16) return W4A16_EINVAL;
+    return H >= 8 && H % 8 == 0 ? W4A16_OK : W4A16_EINVAL;
+}
+
+W4A16_API size_t w4a16_moe_sort_workspace_bytes(int T, int k, int E) {
+    if (check_route(T, k, E) != W4A16_OK) return 0;
+    return route_sort_workspace_bytes(T, k, E, 0);
+}
+
+W4A16_API int w4a16_moe_sort(const int32_t* ids, int T, int k, int E, const void* X, int H, int32_t* offsets,
+                             int32_t* rows, int32_t* slots, void* Xs, void* workspace, size_t ws_bytes,
+                             void* stream) {
+    const int st = check_route(T, k, E);
+    if (st != W4A16_OK) return st;
+    if (!ids || !offsets || !rows || !slots || (X == nullptr) != (Xs == nullptr)) return W4A16_EINVAL;
+    if (X && check_route_rows(W4A16_F16, H) != W4A16_OK) return W4A16_EINVAL;
+    if (!aligned16(ids) || !aligned16(offsets) || !aligned16(rows) || !aligned16(slots) || !aligned16(X) ||
+        !aligned16(Xs))
+        return W4A16_EALIGN;
+    const size_t need = route_sort_workspace_bytes(T, k, E, 0);
+    if (need > 0 && (!workspace || ws_bytes < need)) return W4A16_EWORKSPACE;
+    if (!aligned16(workspace)) return W4A16_EALIGN;
+    RouteSort p = {};
+    p.ids = ids;
+    p.T = T;
+    p.k = k;
+    p.E = E;
+    p.X = X;
+    p.H = X ? H : 8;
+    p.offsets = offsets;
+    p.rows = rows;
+    p.slots = slots;
+    p.Xs = Xs;
+    p.hist = static_cast<int32_t*>(workspace);
+    return launch_route_sort(p, static_cast<cudaStream_t>(stream));
+}
+
+W4A16_API int w4a16_moe_combine(const void* Ys, int dtype, int T, int k, int H, const int32_t* slots,
+                                const float* weights, void* Y, void* stream) {
+    if (check_route(T, k, 1) != W4A16_OK || check_route_rows(dtype, H) != W4A16_OK) return W4A16_EINVAL;
+    if (!Ys || !slots || !Y) return W4A16_EINVAL;
+    if (!aligned16(Ys) || !aligned16(slots) || !aligned16(weights) || !aligned16(Y)) return W4A16_EALIGN;
+    return launch_moe_combine(Ys, dtype, T, k, H, slots, weights, Y, static_cast<cudaStream_t>(stream));
+}
+
+W4A16_API int w4a16_moe_sort_grad(const void* dXs, int dtype, int T, int k, int H, const int32_t* slots, void* dX,
+                                  void* stream) {
+    return w4a16_moe_combine(dXs, dtype, T, k, H, slots, nullptr, dX, stream);
+}
+
+W4A16_API int w4a16_moe_combine_grad(const void* dY, const void* Ys, int dtype, int T, int k, int H,
+                                     const int32_t* slots, const float* weights, void* dYs, float* dweights,
+                                     void* stream) {
+    if (check_route(T, k, 1) != W4A16_OK || check_route_rows(dtype, H) != W4A16_OK) return W4A16_EINVAL;
+    if (!dY || !slots || !dYs || (dweights && !Ys)) return W4A16_EINVAL;
+    if (!aligned16(dY) || !aligned16(Ys) || !aligned16(slots) || !aligned16(weights) || !aligned16(dYs) ||
+        !aligned16(dweights))
+        return W4A16_EALIGN;
+    return launch_moe_combine_grad(dY, Ys, dtype, T, k, H, slots, weights, dYs, dweights,
+                                   static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

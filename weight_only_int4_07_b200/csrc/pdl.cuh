@@ -1,0 +1,30 @@
+// pdl.cuh -- programmatic dependent launch: a kernel may start while the one before it on the
+// stream still runs, and waits for that kernel's results itself.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace w4a16 {
+
+// All kernels before this one on the stream have completed and their writes are visible. A kernel
+// launched with launch_pdl runs it before it touches any buffer that another kernel may use.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next kernel's CTAs may start as this grid's CTAs leave their SMs.
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" :::); }
+
+template <typename... P, typename... A>
+inline cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+}  // namespace w4a16

@@ -1,0 +1,43 @@
+// routed.cuh -- host-side launchers of the routed layers (rows that pick an expert or an adapter).
+#pragma once
+
+#include "common.cuh"
+
+namespace w4a16 {
+
+constexpr int kRouteMaxBins = 1024;      // experts, or adapters
+constexpr int kRouteMaxChoices = 32;     // choices per token
+constexpr int kRouteDirectIds = 8192;    // ids that every CTA counts by itself
+constexpr int kRouteHistIds = 2048;      // ids of one histogram block above that
+
+// A run of up to `rows` consecutive sorted rows that share one bin.
+struct RouteTile {
+    int bin, begin, count, pad;
+};
+
+// Counting sort of n = T k ids into E bins, stable in the flat index: offsets[E + 1], rows (sorted
+// row -> flat index), slots (flat index -> sorted row, -1 without one) and, with X, the gathered rows.
+struct RouteSort {
+    const int32_t* ids;
+    int T, k, E;
+    const void* X;       // [T, H] 16-bit, or null
+    int H;
+    int32_t* offsets;    // null: not written
+    int32_t* rows;
+    int32_t* slots;      // null: not written
+    void* Xs;
+    int32_t* hist;       // route_sort_workspace_bytes
+    int spare;           // ids outside [0, E) go to bin E instead of nowhere (E + 1 bins)
+    RouteTile* tiles;    // null, or the runs of up to tile_rows rows of every bin, in bin order
+    int* ntiles;
+    int tile_rows;
+};
+size_t route_sort_workspace_bytes(int T, int k, int E, int spare);
+int launch_route_sort(const RouteSort& p, cudaStream_t stream);
+
+int launch_moe_combine(const void* Ys, int dtype, int T, int k, int H, const int32_t* slots, const float* weights,
+                       void* Y, cudaStream_t stream);
+int launch_moe_combine_grad(const void* dY, const void* Ys, int dtype, int T, int k, int H, const int32_t* slots,
+                            const float* weights, void* dYs, float* dweights, cudaStream_t stream);
+
+}  // namespace w4a16

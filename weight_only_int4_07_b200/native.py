@@ -80,6 +80,16 @@ def lib():
     L.w4a16_select_kernel.restype = I
     L.w4a16_gemm.argtypes = [P, I, I, I, P, I, P, P, I, I, I, P, P, S, I, P, P]
     L.w4a16_gemm.restype = I
+    L.w4a16_moe_sort_workspace_bytes.argtypes = [I, I, I]
+    L.w4a16_moe_sort_workspace_bytes.restype = S
+    L.w4a16_moe_sort.argtypes = [P, I, I, I, P, I, P, P, P, P, P, S, P]
+    L.w4a16_moe_sort.restype = I
+    L.w4a16_moe_sort_grad.argtypes = [P, I, I, I, I, P, P, P]
+    L.w4a16_moe_sort_grad.restype = I
+    L.w4a16_moe_combine.argtypes = [P, I, I, I, I, P, P, P, P]
+    L.w4a16_moe_combine.restype = I
+    L.w4a16_moe_combine_grad.argtypes = [P, P, I, I, I, I, P, P, P, P, P]
+    L.w4a16_moe_combine_grad.restype = I
     L.w4a16_status_str.argtypes = [I]
     L.w4a16_status_str.restype = ctypes.c_char_p
     L.w4a16_version.argtypes = []
@@ -303,3 +313,129 @@ def w4a16_gemm_noalloc(A, codes, scales, zeros, N, group, sym, C=None):
                               N, group, int(sym), _ptr(C), _stream())
     _check("w4a16_gemm_noalloc", st)
     return C
+
+
+# ----------------------------------------------------------------------------- routed layers
+def _need(fn, ok):
+    if not ok:
+        raise W4A16Error(fn, EINVAL)
+
+
+def _arg(fn, t, dtype, shape, dev):
+    """The address of a contiguous CUDA tensor of this type and shape on device `dev` (its index)."""
+    _need(fn, t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev)
+    return t.data_ptr()
+
+
+def _out(fn, t, dtype, shape, dev):
+    """`t`, checked, or a new tensor of this type and shape."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    _arg(fn, t, dtype, shape, dev)
+    return t
+
+
+def _room(fn, t, nbytes, dev, zeroed=False):
+    """A caller's workspace, checked, or a new one."""
+    if t is None:
+        make = torch.zeros if zeroed else torch.empty
+        return make(nbytes, dtype=torch.uint8, device=torch.device("cuda", dev))
+    _need(fn, t.is_contiguous() and t.get_device() == dev)
+    return t
+
+
+def _call(name, dev, *args):
+    """One entry point on the current stream of device `dev`, with that device current."""
+    f = getattr(lib(), name)
+    if dev == torch.cuda.current_device():
+        st = f(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, torch.cuda.current_stream().cuda_stream)
+    if st != OK:
+        raise W4A16Error(name, st)
+
+
+def _dev(fn, t):
+    _need(fn, t.is_cuda)
+    return t.get_device()
+
+
+def w4a16_moe_sort_workspace_bytes(T, k, n_experts) -> int:
+    return int(lib().w4a16_moe_sort_workspace_bytes(T, k, n_experts))
+
+
+def w4a16_moe_sort(ids, n_experts, X=None, offsets=None, rows=None, slots=None, Xs=None, workspace=None):
+    """Tokens sorted by expert: ids int32 [T, k] (and the tokens' 16-bit rows X [T, H]) ->
+    (offsets [E + 1], rows [T k], slots [T, k], Xs [T k, H] or None). Entries of `rows` and rows of
+    `Xs` at or past offsets[E] are left as they were."""
+    fn = "w4a16_moe_sort"
+    dev = _dev(fn, ids)
+    _need(fn, ids.dim() == 2)
+    T, k = ids.shape
+    _need(fn, T > 0 and k > 0 and n_experts > 0 and (X is not None or Xs is None))
+    i32 = torch.int32
+    p = _arg(fn, ids, i32, (T, k), dev)
+    offsets = _out(fn, offsets, i32, (n_experts + 1,), dev)
+    rows = _out(fn, rows, i32, (T * k,), dev)
+    slots = _out(fn, slots, i32, (T, k), dev)
+    H = 0
+    if X is not None:
+        _need(fn, X.dim() == 2 and X.dtype in _DTYPES)
+        H = X.shape[1]
+        px = _arg(fn, X, X.dtype, (T, H), dev)
+        Xs = _out(fn, Xs, X.dtype, (T * k, H), dev)
+    need = w4a16_moe_sort_workspace_bytes(T, k, n_experts)
+    pw, nb = None, 0
+    if need > 0:
+        workspace = _room(fn, workspace, need, dev)
+        pw, nb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call(fn, dev, p, T, k, n_experts, px if H else None, H, offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(),
+          Xs.data_ptr() if H else None, pw, nb)
+    return offsets, rows, slots, Xs
+
+
+def _sum_rows(fn, Ys, slots, weights, Y):
+    dev = _dev(fn, Ys)
+    _need(fn, slots.dim() == 2 and Ys.dim() == 2 and Ys.dtype in _DTYPES)
+    (T, k), H, t = slots.shape, Ys.shape[1], Ys.dtype
+    ps = _arg(fn, slots, torch.int32, (T, k), dev)
+    py = _arg(fn, Ys, t, (T * k, H), dev)
+    Y = _out(fn, Y, t, (T, H), dev)
+    if fn == "w4a16_moe_sort_grad":
+        _call(fn, dev, py, _DTYPES[t], T, k, H, ps, Y.data_ptr())
+    else:
+        pw = None if weights is None else _arg(fn, weights, torch.float32, (T, k), dev)
+        _call(fn, dev, py, _DTYPES[t], T, k, H, ps, pw, Y.data_ptr())
+    return Y
+
+
+def w4a16_moe_combine(Ys, slots, weights=None, Y=None):
+    """Y[t] = sum_j weights[t, j] Ys[slots[t, j]] for 16-bit sorted rows Ys [T k, H], slots int32
+    [T, k] and fp32 weights [T, k] (None: all 1); FP32 sums, Y [T, H] in the type of Ys."""
+    return _sum_rows("w4a16_moe_combine", Ys, slots, weights, Y)
+
+
+def w4a16_moe_sort_grad(dXs, slots, dX=None):
+    """The gradient of w4a16_moe_sort's gather: dX[t] = sum_j dXs[slots[t, j]]."""
+    return _sum_rows("w4a16_moe_sort_grad", dXs, slots, None, dX)
+
+
+def w4a16_moe_combine_grad(dY, Ys, slots, weights=None, dYs=None, dweights=None):
+    """The gradient of w4a16_moe_combine -> (dYs [T k, H], dweights fp32 [T, k]); Ys None: dYs
+    alone (dweights None). Rows of dYs without a choice are left as they were."""
+    fn = "w4a16_moe_combine_grad"
+    dev = _dev(fn, dY)
+    _need(fn, slots.dim() == 2 and dY.dim() == 2 and dY.dtype in _DTYPES and (Ys is not None or dweights is None))
+    (T, k), H, t = slots.shape, dY.shape[1], dY.dtype
+    ps = _arg(fn, slots, torch.int32, (T, k), dev)
+    pg = _arg(fn, dY, t, (T, H), dev)
+    pw = None if weights is None else _arg(fn, weights, torch.float32, (T, k), dev)
+    dYs = _out(fn, dYs, t, (T * k, H), dev)
+    py = None
+    if Ys is not None:
+        py = _arg(fn, Ys, t, (T * k, H), dev)
+        dweights = _out(fn, dweights, torch.float32, (T, k), dev)
+    _call(fn, dev, pg, py, _DTYPES[t], T, k, H, ps, pw, dYs.data_ptr(),
+          None if dweights is None else dweights.data_ptr())
+    return dYs, dweights
