@@ -421,6 +421,35 @@ W4A16_API int w4a16_moe_combine_grad(const void* dY, const void* Ys, int dtype, 
                                      void* stream);
 
 /*
+ * w4a16_moe_gemm -- the experts' INT4 products on sorted rows: C[i] = A[i] . dequant(W_e) for
+ *   offsets[e] <= i < offsets[e + 1], e < E, FP32 accumulation, C in the dtype of A. The offsets are
+ *   read on the device, so the call needs no host knowledge of the routing and can be captured.
+ * Arguments
+ *   A          device, [R, K] row-major, fp16 or bf16 (a_dtype): the sorted rows (w4a16_moe_sort's Xs,
+ *              R = T k). R >= 1 is the room of A and C; rows at or past offsets[E] are not used.
+ *   tiled      device: E buffers of w4a16_repack, one per expert, w4a16_repack_bytes(K, N, group, sym)
+ *              apart. K % 128 == 0 and N % 128 == 0 (else W4A16_EUNSUPPORTED).
+ *   E          experts, 1 to 1024.
+ *   offsets    device, int32 [E + 1], not decreasing, offsets[E] <= R. Values outside [0, R] are
+ *              clamped to it and a run that ends before it begins is empty: no value reads or
+ *              writes outside the buffers. Rows of C outside every run are left as they were.
+ *   N, group, sym   as for w4a16_gemm; the same for every expert.
+ *   C          device out, [R, N] row-major, dtype a_dtype. Must not overlap an input.
+ *   workspace, ws_bytes   device, at least w4a16_moe_workspace_bytes(R, E, N, K, group) bytes, 16-byte
+ *              aligned, under the contract of w4a16_gemm's workspace (first 64 KiB zero before the
+ *              first call; calls that share one ordered on the GPU; zeroed again after
+ *              W4A16_ETIMEOUT). It may be shared with w4a16_gemm.
+ *   kernel     W4A16_KERNEL_AUTO, or a forced W4A16_KERNEL_GEMV or W4A16_KERNEL_TC.
+ *   dev_status device int or NULL: W4A16_ETIMEOUT as for w4a16_gemm.
+ *   stream     cudaStream_t. One kernel launch.
+ * Returns W4A16_OK, W4A16_EINVAL, W4A16_EALIGN, W4A16_EUNSUPPORTED, W4A16_EWORKSPACE or W4A16_ECUDA.
+ */
+W4A16_API size_t w4a16_moe_workspace_bytes(int R, int E, int N, int K, int group);
+W4A16_API int w4a16_moe_gemm(const void* A, int a_dtype, int R, int K, const void* tiled, int E,
+                             const int32_t* offsets, int N, int group, int sym, void* C, void* workspace,
+                             size_t ws_bytes, int kernel, int* dev_status, void* stream);
+
+/*
  * w4a16_set_wait_limit_ns -- the time limit of every bounded wait inside the library's kernels
  *   (a pipeline barrier, or a counter another CTA of the same launch sets), in nanoseconds, for
  *   launches made after the call; 0 restores the default of 2 s. Returns the previous limit.

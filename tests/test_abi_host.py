@@ -356,3 +356,35 @@ def test_routed_binding_refuses_what_does_not_fit():
         with pytest.raises(native.W4A16Error) as e:
             call()
         assert e.value.status == native.EINVAL
+
+
+def test_moe_gemm_rejects_bad_arguments_before_any_launch(L):
+    P = ctypes.c_void_p
+    A, W, off, C, ws = (P((i + 1) << 20) for i in range(5))
+    mis = P((9 << 20) + 8)
+    R, E, N, K, g = 64, 8, 256, 512, 128
+    need = native.w4a16_moe_workspace_bytes(R, E, N, K, g)
+    assert need >= 65536
+    assert native.w4a16_moe_workspace_bytes(0, E, N, K, g) == 0
+    assert native.w4a16_moe_workspace_bytes(R, 1025, N, K, g) == 0
+    assert native.w4a16_moe_workspace_bytes(R, E, 200, K, g) == 0
+
+    def call(A=A, dt=0, R=R, K=K, W=W, E=E, off=off, N=N, g=g, sym=0, C=C, ws=ws, wsb=need, kernel=0):
+        return L.w4a16_moe_gemm(A, dt, R, K, W, E, off, N, g, sym, C, ws, wsb, kernel, None, None)
+    assert call(R=0) == native.EINVAL
+    assert call(E=0) == native.EINVAL
+    assert call(E=1025) == native.EINVAL
+    assert call(K=500) == native.EINVAL
+    assert call(K=192, g=64) == native.EUNSUPPORTED            # tiles of 128 input channels
+    assert call(N=136) == native.EUNSUPPORTED
+    assert call(g=16) == native.EUNSUPPORTED
+    assert call(dt=2) == native.EINVAL
+    assert call(sym=2) == native.EINVAL
+    assert call(kernel=5) == native.EINVAL
+    assert call(off=None) == native.EINVAL
+    assert call(W=None) == native.EINVAL
+    assert call(A=mis) == native.EALIGN
+    assert call(off=mis) == native.EALIGN
+    assert call(ws=None) == native.EWORKSPACE
+    assert call(wsb=need - 1) == native.EWORKSPACE
+    assert call(ws=mis) == native.EALIGN

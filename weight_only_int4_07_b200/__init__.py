@@ -23,9 +23,11 @@ from .native import (  # noqa: F401
     w4a16_gptq_workspace_bytes,
     w4a16_moe_combine,
     w4a16_moe_combine_grad,
+    w4a16_moe_gemm,
     w4a16_moe_sort,
     w4a16_moe_sort_grad,
     w4a16_moe_sort_workspace_bytes,
+    w4a16_moe_workspace_bytes,
     w4a16_quantize,
     w4a16_repack,
     w4a16_repack_bytes,

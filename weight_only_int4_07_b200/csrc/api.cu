@@ -376,4 +376,34 @@ W4A16_API int w4a16_moe_combine_grad(const void* dY, const void* Ys, int dtype, 
                                    static_cast<cudaStream_t>(stream));
 }
 
+static int check_moe_gemm(int R, int E, int N, int K, int group) {
+    const int st = check_shape(K, N, group);
+    if (st != W4A16_OK) return st;
+    if (R < 1 || E < 1 || E > kRouteMaxBins) return W4A16_EINVAL;
+    return N % kTileN == 0 && K % kTileK == 0 ? W4A16_OK : W4A16_EUNSUPPORTED;
+}
+
+W4A16_API size_t w4a16_moe_workspace_bytes(int R, int E, int N, int K, int group) {
+    if (check_moe_gemm(R, E, N, K, group) != W4A16_OK) return 0;
+    return kGemvStreamCounterBytes + moe_gemm_partial_bytes(R, E, N, K, group);
+}
+
+W4A16_API int w4a16_moe_gemm(const void* A, int a_dtype, int R, int K, const void* tiled, int E,
+                             const int32_t* offsets, int N, int group, int sym, void* C, void* workspace,
+                             size_t ws_bytes, int kernel, int* dev_status, void* stream) {
+    const int st = check_moe_gemm(R, E, N, K, group);
+    if (st != W4A16_OK) return st;
+    if (a_dtype != W4A16_F16 && a_dtype != W4A16_BF16) return W4A16_EINVAL;
+    if (sym != 0 && sym != 1) return W4A16_EINVAL;
+    if (kernel != W4A16_KERNEL_AUTO && kernel != W4A16_KERNEL_GEMV && kernel != W4A16_KERNEL_TC) return W4A16_EINVAL;
+    if (!A || !tiled || !offsets || !C) return W4A16_EINVAL;
+    if (!aligned16(A) || !aligned16(tiled) || !aligned16(offsets) || !aligned16(C)) return W4A16_EALIGN;
+    if (!workspace || ws_bytes < w4a16_moe_workspace_bytes(R, E, N, K, group)) return W4A16_EWORKSPACE;
+    if (!aligned16(workspace)) return W4A16_EALIGN;
+    if (log_enabled())
+        fprintf(stderr, "[w4a16] moe gemm R=%d E=%d N=%d K=%d g=%d sym=%d\n", R, E, N, K, group, sym);
+    return launch_moe_gemm(A, a_dtype, R, K, tiled, E, offsets, N, group, sym, C, workspace, kernel, dev_status,
+                           static_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"

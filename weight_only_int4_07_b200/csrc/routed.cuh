@@ -1,6 +1,8 @@
 // routed.cuh -- host-side launchers of the routed layers (rows that pick an expert or an adapter).
 #pragma once
 
+#include <cuda.h>
+
 #include "common.cuh"
 
 namespace w4a16 {
@@ -39,5 +41,14 @@ int launch_moe_combine(const void* Ys, int dtype, int T, int k, int H, const int
                        void* Y, cudaStream_t stream);
 int launch_moe_combine_grad(const void* dY, const void* Ys, int dtype, int T, int k, int H, const int32_t* slots,
                             const float* weights, void* dYs, float* dweights, cudaStream_t stream);
+
+// Shared with the dense tensor-core GEMM (gemm_tc.cu).
+bool make_act_map(CUtensorMap* map, const void* A, int M, int K, int box_rows, bool bf16);
+TcPlan plan_tc_rows(int bn, int N, int K, int group, int sym, int ctas, size_t table);
+
+// The experts' products on R sorted rows: workspace after the counters, and the launch.
+size_t moe_gemm_partial_bytes(int R, int E, int N, int K, int group);
+int launch_moe_gemm(const void* A, int a_dtype, int R, int K, const void* tiled, int E, const int32_t* offsets, int N,
+                    int group, int sym, void* C, void* workspace, int kernel, int* dev_status, cudaStream_t stream);
 
 }  // namespace w4a16

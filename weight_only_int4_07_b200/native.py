@@ -90,6 +90,10 @@ def lib():
     L.w4a16_moe_combine.restype = I
     L.w4a16_moe_combine_grad.argtypes = [P, P, I, I, I, I, P, P, P, P, P]
     L.w4a16_moe_combine_grad.restype = I
+    L.w4a16_moe_workspace_bytes.argtypes = [I, I, I, I, I]
+    L.w4a16_moe_workspace_bytes.restype = S
+    L.w4a16_moe_gemm.argtypes = [P, I, I, I, P, I, P, I, I, I, P, P, S, I, P, P]
+    L.w4a16_moe_gemm.restype = I
     L.w4a16_status_str.argtypes = [I]
     L.w4a16_status_str.restype = ctypes.c_char_p
     L.w4a16_version.argtypes = []
@@ -356,6 +360,10 @@ def _call(name, dev, *args):
         raise W4A16Error(name, st)
 
 
+def _status_arg(fn, t, dev):
+    return None if t is None else _arg(fn, t, torch.int32, t.shape, dev)
+
+
 def _dev(fn, t):
     _need(fn, t.is_cuda)
     return t.get_device()
@@ -439,3 +447,27 @@ def w4a16_moe_combine_grad(dY, Ys, slots, weights=None, dYs=None, dweights=None)
     _call(fn, dev, pg, py, _DTYPES[t], T, k, H, ps, pw, dYs.data_ptr(),
           None if dweights is None else dweights.data_ptr())
     return dYs, dweights
+
+
+def w4a16_moe_workspace_bytes(R, n_experts, N, K, group) -> int:
+    return int(lib().w4a16_moe_workspace_bytes(R, n_experts, N, K, group))
+
+
+def w4a16_moe_gemm(A, offsets, tiled, N, group, sym, C=None, workspace=None, kernel=KERNEL_AUTO, dev_status=None):
+    """C[i] = A[i] . dequant(W_e), offsets[e] <= i < offsets[e + 1], for 16-bit sorted rows A [R, K],
+    int32 offsets [E + 1] and uint8 tiled [E, w4a16_repack_bytes(K, N, group, sym)]. Rows of C outside
+    every run are left as they were. A workspace may be kept: zeros at first, one per stream."""
+    fn = "w4a16_moe_gemm"
+    dev = _dev(fn, A)
+    _need(fn, A.dim() == 2 and A.dtype in _DTYPES and offsets.dim() == 1)
+    (R, K), E, t = A.shape, offsets.shape[0] - 1, A.dtype
+    pa = _arg(fn, A, t, (R, K), dev)
+    po = _arg(fn, offsets, torch.int32, (E + 1,), dev)
+    pw = _arg(fn, tiled, torch.uint8, (E, w4a16_repack_bytes(K, N, group, sym)), dev)
+    C = _out(fn, C, t, (R, N), dev)
+    if workspace is None:
+        workspace = _room(fn, None, w4a16_moe_workspace_bytes(R, E, N, K, group), dev, zeroed=True)
+    _call(fn, dev, pa, _DTYPES[t], R, K, pw, E, po, N, group, int(sym), C.data_ptr(),
+          _room(fn, workspace, 0, dev).data_ptr(), workspace.numel() * workspace.element_size(), int(kernel),
+          _status_arg(fn, dev_status, dev))
+    return C
