@@ -450,6 +450,37 @@ W4A16_API int w4a16_moe_gemm(const void* A, int a_dtype, int R, int K, const voi
                              size_t ws_bytes, int kernel, int* dev_status, void* stream);
 
 /*
+ * w4a16_lora_gemm -- the layer with low-rank adapters of many requests at once:
+ *   C[m] = A[m] . dequant(W) + scale_a (A[m] . La_a^T) . Lb_a^T,  a = row_adapter[m],
+ *   the first term alone where row_adapter[m] is outside [0, adapters). All sums in FP32, C rounded
+ *   once. Rows that share an adapter share its reads; nothing depends on their order.
+ * Arguments
+ *   A, a_dtype, M, K, tiled, N, group, sym   as for w4a16_gemm on the TILED layout (K and N multiples of
+ *              128, else W4A16_EUNSUPPORTED).
+ *   lora_a     device, a_dtype [adapters, rank, K] row-major (La).
+ *   lora_b     device, a_dtype [adapters, N, rank] row-major (Lb).
+ *   lora_scale device, fp32 [adapters].
+ *   adapters   1 to 1024. Adapters of smaller rank are padded with zeros.
+ *   rank       8 to 256, a multiple of 8 (above: W4A16_EUNSUPPORTED).
+ *   row_adapter   device, int32 [M].
+ *   C          device out, [M, N] row-major, dtype a_dtype. Must not overlap an input.
+ *   workspace, ws_bytes   device, at least w4a16_lora_workspace_bytes(M, N, K, group, rank, adapters)
+ *              bytes, 16-byte aligned, under the contract of w4a16_gemm's workspace. It may be
+ *              shared with w4a16_gemm. It holds the FP32 outputs of at most 64 MiB or 256 rows at a
+ *              time, whichever is more; longer batches are taken in pieces.
+ *   dev_status device int or NULL: W4A16_ETIMEOUT as for w4a16_gemm.
+ *   stream     cudaStream_t. Three kernel launches up to 16 rows, four above (each piece).
+ * The weight buffer must not be written by the kernel that immediately precedes the call (see
+ * w4a16_gemm, "Ordering").
+ * Returns W4A16_OK, W4A16_EINVAL, W4A16_EALIGN, W4A16_EUNSUPPORTED, W4A16_EWORKSPACE or W4A16_ECUDA.
+ */
+W4A16_API size_t w4a16_lora_workspace_bytes(int M, int N, int K, int group, int rank, int adapters);
+W4A16_API int w4a16_lora_gemm(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
+                              const void* lora_a, const void* lora_b, const float* lora_scale, int adapters,
+                              int rank, const int32_t* row_adapter, void* C, void* workspace, size_t ws_bytes,
+                              int* dev_status, void* stream);
+
+/*
  * w4a16_set_wait_limit_ns -- the time limit of every bounded wait inside the library's kernels
  *   (a pipeline barrier, or a counter another CTA of the same launch sets), in nanoseconds, for
  *   launches made after the call; 0 restores the default of 2 s. Returns the previous limit.

@@ -48,3 +48,21 @@ def combine_grad(dY, Ys, slots, weights):
                 dw[t, j] = dY[t] @ Ys[s]
                 dwabs[t, j] = np.abs(dY[t]) @ np.abs(Ys[s])
     return dYs, dw, dwabs
+
+
+def lora(A, La, Lb, scale, row_adapter):
+    """The adapters' term of the layer, delta [M, N], and the magnitudes an error bound needs: per
+    output sum_j |s T_j Lb_nj|, sum_j |s Lb_nj| sum_k |A_k La_jk| and max_j |s T_j| sum_j |Lb_nj|."""
+    M, N = A.shape[0], Lb.shape[1]
+    out = [np.zeros((M, N)) for _ in range(4)]
+    for m in range(M):
+        a = int(row_adapter[m])
+        if not 0 <= a < La.shape[0]:
+            continue
+        s = float(scale[a])
+        T = La[a] @ A[m]
+        out[0][m] = s * (Lb[a] @ T)
+        out[1][m] = abs(s) * (np.abs(Lb[a]) @ np.abs(T))
+        out[2][m] = abs(s) * (np.abs(Lb[a]) @ (np.abs(La[a]) @ np.abs(A[m])))
+        out[3][m] = abs(s) * np.abs(T).max() * np.abs(Lb[a]).sum(1)
+    return out

@@ -388,3 +388,37 @@ def test_moe_gemm_rejects_bad_arguments_before_any_launch(L):
     assert call(ws=None) == native.EWORKSPACE
     assert call(wsb=need - 1) == native.EWORKSPACE
     assert call(ws=mis) == native.EALIGN
+
+
+def test_lora_rejects_bad_arguments_before_any_launch(L):
+    P = ctypes.c_void_p
+    A, W, la, lb, sc, ids, C, ws = (P((i + 1) << 20) for i in range(8))
+    mis = P((9 << 20) + 8)
+    M, N, K, g, r, n = 4, 256, 512, 128, 16, 8
+    need = native.w4a16_lora_workspace_bytes(M, N, K, g, r, n)
+    assert need >= native.w4a16_workspace_bytes(M, N, K, g) + M * N * 4
+    assert native.w4a16_lora_workspace_bytes(M, N, K, g, 12, n) == 0
+    assert native.w4a16_lora_workspace_bytes(M, N, K, g, r, 0) == 0
+    # the FP32 outputs of a long batch are held in pieces
+    assert native.w4a16_lora_workspace_bytes(1 << 20, 28672, 4096, g, r, n) < (1 << 28)
+
+    def call(A=A, dt=0, M=M, K=K, W=W, N=N, g=g, sym=0, la=la, lb=lb, sc=sc, n=n, r=r, ids=ids, C=C, ws=ws, wsb=need):
+        return L.w4a16_lora_gemm(A, dt, M, K, W, N, g, sym, la, lb, sc, n, r, ids, C, ws, wsb, None, None)
+    assert call(M=0) == native.EINVAL
+    assert call(K=500) == native.EINVAL
+    assert call(K=192, g=64) == native.EUNSUPPORTED
+    assert call(N=136) == native.EUNSUPPORTED
+    assert call(r=0) == native.EINVAL
+    assert call(r=12) == native.EINVAL
+    assert call(r=264) == native.EUNSUPPORTED
+    assert call(n=0) == native.EINVAL
+    assert call(n=1025) == native.EINVAL
+    assert call(dt=3) == native.EINVAL
+    assert call(sym=-1) == native.EINVAL
+    assert call(la=None) == native.EINVAL
+    assert call(ids=None) == native.EINVAL
+    assert call(lb=mis) == native.EALIGN
+    assert call(ids=mis) == native.EALIGN
+    assert call(ws=None) == native.EWORKSPACE
+    assert call(wsb=need - 1) == native.EWORKSPACE
+    assert call(ws=mis) == native.EALIGN

@@ -58,3 +58,16 @@ def test_combine_grad_matches_differences():
             b[s, h] -= 0.5
             want = dYs[s][h] if s in dYs else 0.0
             assert abs(loss(a, w) - loss(b, w) - want) < 1e-12
+
+
+def test_lora_is_the_merged_weight():
+    """A row of adapter a sees the weight s La_a^T Lb_a^T; rows without one see none."""
+    rng = np.random.default_rng(5)
+    M, K, N, r, L = 6, 12, 10, 4, 3
+    A, La, Lb = rng.standard_normal((M, K)), rng.standard_normal((L, r, K)), rng.standard_normal((L, N, r))
+    scale, ids = rng.standard_normal(L), np.array([0, 2, -1, 1, 3, 2])
+    delta, mag, mag2, _ = routed.lora(A, La, Lb, scale, ids)
+    for m, a in enumerate(ids):
+        want = A[m] @ (scale[a] * La[a].T @ Lb[a].T) if 0 <= a < L else np.zeros(N)
+        assert np.allclose(delta[m], want, rtol=1e-12, atol=1e-12)
+        assert (np.abs(delta[m]) <= mag[m] + 1e-12).all() and (mag[m] <= mag2[m] + 1e-12).all()

@@ -406,4 +406,50 @@ W4A16_API int w4a16_moe_gemm(const void* A, int a_dtype, int R, int K, const voi
                            static_cast<cudaStream_t>(stream));
 }
 
+static int check_lora(int M, int N, int K, int group, int rank, int adapters) {
+    const int st = check_shape(K, N, group);
+    if (st != W4A16_OK) return st;
+    if (M < 1 || adapters < 1 || adapters > kRouteMaxBins) return W4A16_EINVAL;
+    if (rank < 8 || rank % 8 != 0) return W4A16_EINVAL;
+    if (rank > kLoraMaxRank) return W4A16_EUNSUPPORTED;
+    return N % kTileN == 0 && K % kTileK == 0 ? W4A16_OK : W4A16_EUNSUPPORTED;
+}
+
+W4A16_API size_t w4a16_lora_workspace_bytes(int M, int N, int K, int group, int rank, int adapters) {
+    if (check_lora(M, N, K, group, rank, adapters) != W4A16_OK) return 0;
+    return lora_workspace_bytes(M, N, K, group, rank, adapters);
+}
+
+W4A16_API int w4a16_lora_gemm(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
+                              const void* lora_a, const void* lora_b, const float* lora_scale, int adapters,
+                              int rank, const int32_t* row_adapter, void* C, void* workspace, size_t ws_bytes,
+                              int* dev_status, void* stream) {
+    const int st = check_lora(M, N, K, group, rank, adapters);
+    if (st != W4A16_OK) return st;
+    if (a_dtype != W4A16_F16 && a_dtype != W4A16_BF16) return W4A16_EINVAL;
+    if (sym != 0 && sym != 1) return W4A16_EINVAL;
+    if (!A || !tiled || !lora_a || !lora_b || !lora_scale || !row_adapter || !C) return W4A16_EINVAL;
+    if (!aligned16(A) || !aligned16(tiled) || !aligned16(lora_a) || !aligned16(lora_b) || !aligned16(lora_scale) ||
+        !aligned16(row_adapter) || !aligned16(C))
+        return W4A16_EALIGN;
+    if (!workspace || ws_bytes < lora_workspace_bytes(M, N, K, group, rank, adapters)) return W4A16_EWORKSPACE;
+    if (!aligned16(workspace)) return W4A16_EALIGN;
+    if (log_enabled())
+        fprintf(stderr, "[w4a16] lora gemm M=%d N=%d K=%d g=%d sym=%d rank=%d adapters=%d\n", M, N, K, group, sym,
+                rank, adapters);
+    return launch_lora_gemm(A, a_dtype, M, K, tiled, N, group, sym, lora_a, lora_b, lora_scale, adapters, rank,
+                            row_adapter, C, workspace, dev_status, static_cast<cudaStream_t>(stream));
+}
+
 }  // extern "C"
+
+int w4a16::launch_gemm_f32(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
+                           float* y, int* slices, void* workspace, int* dev_status, cudaStream_t stream) {
+    if (w4a16_select_kernel(M, N, K, group) == W4A16_KERNEL_GEMV) {
+        const int st = launch_gemv_stream_f32(A, a_dtype, M, K, tiled, N, group, sym, y, slices, workspace, dev_status,
+                                              stream);
+        if (st != W4A16_EUNSUPPORTED) return st;
+    }
+    *slices = 1;
+    return launch_gemm_tc_f32(A, a_dtype, M, K, tiled, N, group, sym, y, workspace, dev_status, stream);
+}

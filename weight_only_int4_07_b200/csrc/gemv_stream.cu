@@ -52,6 +52,7 @@
 
 #include "common.cuh"
 #include "dequant.cuh"
+#include "routed.cuh"
 #include "sm100_ptx.cuh"
 #include "tiled_layout.cuh"
 
@@ -834,8 +835,9 @@ GemvStreamPlan plan_gemv_stream(int M, int N, int K, int group, int sym, int n_s
 
 int gemv_stream_sm_count() { return sm_count(); }
 
-int launch_gemv_stream(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
-                       void* C, void* workspace, int* dev_status, cudaStream_t stream) {
+// y32: FP32 outputs of the S slices ([S][M][N], S >= 1) instead of C; slices gets S.
+static int launch_gemv(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym, void* C,
+                       float* y32, int* slices, void* workspace, int* dev_status, cudaStream_t stream) {
     const GemvStreamPlan pl = plan_gemv_stream(M, N, K, group, sym, sm_count());
     if (!pl.ok) return W4A16_EUNSUPPORTED;
     if (!workspace) return W4A16_EWORKSPACE;
@@ -880,11 +882,12 @@ int launch_gemv_stream(const void* A, int a_dtype, int M, int K, const void* til
     prm.A = A;
     prm.c0 = 0;
     prm.slices = S;
-    prm.out_f32 = S > 1 ? slice_out : nullptr;
+    prm.out_f32 = y32 ? y32 : S > 1 ? slice_out : nullptr;
+    if (slices) *slices = S;
     const int st = bf16 ? launch_rows<__nv_bfloat16>(prm, group, pl.smem, stream)
                         : launch_rows<__half>(prm, group, pl.smem, stream);
     if (st != W4A16_OK) return st;
-    if (S > 1) {
+    if (S > 1 && !y32) {
         const size_t MN = (size_t)M * N;
         const unsigned blocks = (unsigned)((MN + 255) / 256 < 2048 ? (MN + 255) / 256 : 2048);
         if (bf16)
@@ -895,6 +898,16 @@ int launch_gemv_stream(const void* A, int a_dtype, int M, int K, const void* til
         return launch_status();
     }
     return W4A16_OK;
+}
+
+int launch_gemv_stream(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
+                       void* C, void* workspace, int* dev_status, cudaStream_t stream) {
+    return launch_gemv(A, a_dtype, M, K, tiled, N, group, sym, C, nullptr, nullptr, workspace, dev_status, stream);
+}
+
+int launch_gemv_stream_f32(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
+                           float* y, int* slices, void* workspace, int* dev_status, cudaStream_t stream) {
+    return launch_gemv(A, a_dtype, M, K, tiled, N, group, sym, nullptr, y, slices, workspace, dev_status, stream);
 }
 
 }  // namespace w4a16

@@ -51,4 +51,21 @@ size_t moe_gemm_partial_bytes(int R, int E, int N, int K, int group);
 int launch_moe_gemm(const void* A, int a_dtype, int R, int K, const void* tiled, int E, const int32_t* offsets, int N,
                     int group, int sym, void* C, void* workspace, int kernel, int* dev_status, cudaStream_t stream);
 
+// The dense layer with FP32 outputs y [slices][M][N] (to be added up), chosen as w4a16_gemm chooses:
+// the decode kernel (launch_gemv_stream_f32, gemv_stream.cu) or the tensor-core GEMM
+// (launch_gemm_tc_f32, gemm_tc_f32.cu). `workspace` under the contract of w4a16_gemm.
+int launch_gemv_stream_f32(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
+                           float* y, int* slices, void* workspace, int* dev_status, cudaStream_t stream);
+int launch_gemm_tc_f32(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
+                       float* y, void* workspace, int* dev_status, cudaStream_t stream);
+int launch_gemm_f32(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym, float* y,
+                    int* slices, void* workspace, int* dev_status, cudaStream_t stream);
+
+// The layer with low-rank adapters.
+constexpr int kLoraMaxRank = 256;
+size_t lora_workspace_bytes(int M, int N, int K, int group, int rank, int adapters);
+int launch_lora_gemm(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
+                     const void* La, const void* Lb, const float* scale, int adapters, int rank,
+                     const int32_t* row_adapter, void* C, void* workspace, int* dev_status, cudaStream_t stream);
+
 }  // namespace w4a16

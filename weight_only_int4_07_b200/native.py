@@ -94,6 +94,10 @@ def lib():
     L.w4a16_moe_workspace_bytes.restype = S
     L.w4a16_moe_gemm.argtypes = [P, I, I, I, P, I, P, I, I, I, P, P, S, I, P, P]
     L.w4a16_moe_gemm.restype = I
+    L.w4a16_lora_workspace_bytes.argtypes = [I, I, I, I, I, I]
+    L.w4a16_lora_workspace_bytes.restype = S
+    L.w4a16_lora_gemm.argtypes = [P, I, I, I, P, I, I, I, P, P, P, I, I, P, P, P, S, P, P]
+    L.w4a16_lora_gemm.restype = I
     L.w4a16_status_str.argtypes = [I]
     L.w4a16_status_str.restype = ctypes.c_char_p
     L.w4a16_version.argtypes = []
@@ -348,14 +352,21 @@ def _room(fn, t, nbytes, dev, zeroed=False):
     return t
 
 
+def _raw_stream(dev):
+    """The current stream of device `dev` as a cudaStream_t (torch.cuda.current_stream builds a Python
+    object on the way, 3 us of a small call)."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
 def _call(name, dev, *args):
     """One entry point on the current stream of device `dev`, with that device current."""
     f = getattr(lib(), name)
+    stream = _raw_stream(dev)
     if dev == torch.cuda.current_device():
-        st = f(*args, torch.cuda.current_stream().cuda_stream)
+        st = f(*args, stream)
     else:
         with torch.cuda.device(dev):
-            st = f(*args, torch.cuda.current_stream().cuda_stream)
+            st = f(*args, stream)
     if st != OK:
         raise W4A16Error(name, st)
 
@@ -469,5 +480,34 @@ def w4a16_moe_gemm(A, offsets, tiled, N, group, sym, C=None, workspace=None, ker
         workspace = _room(fn, None, w4a16_moe_workspace_bytes(R, E, N, K, group), dev, zeroed=True)
     _call(fn, dev, pa, _DTYPES[t], R, K, pw, E, po, N, group, int(sym), C.data_ptr(),
           _room(fn, workspace, 0, dev).data_ptr(), workspace.numel() * workspace.element_size(), int(kernel),
+          _status_arg(fn, dev_status, dev))
+    return C
+
+
+def w4a16_lora_workspace_bytes(M, N, K, group, rank, adapters) -> int:
+    return int(lib().w4a16_lora_workspace_bytes(M, N, K, group, rank, adapters))
+
+
+def w4a16_lora_gemm(A, tiled, N, group, sym, lora_a, lora_b, lora_scale, row_adapter, C=None, workspace=None,
+                    dev_status=None):
+    """C[m] = A[m] . dequant(W) + lora_scale[a] (A[m] . lora_a[a]^T) . lora_b[a]^T, a = row_adapter[m]
+    (outside [0, L): the first term alone). 16-bit A [M, K], lora_a [L, r, K], lora_b [L, N, r] of one
+    type, tiled uint8 (w4a16_repack), lora_scale fp32 [L], row_adapter int32 [M]; FP32 sums, rounded once.
+    A workspace may be kept: zeros at first, one per stream."""
+    fn = "w4a16_lora_gemm"
+    dev = _dev(fn, A)
+    _need(fn, A.dim() == 2 and A.dtype in _DTYPES and lora_a.dim() == 3)
+    (M, K), (L, r, _), t = A.shape, lora_a.shape, A.dtype
+    pa = _arg(fn, A, t, (M, K), dev)
+    pw = _arg(fn, tiled, torch.uint8, (w4a16_repack_bytes(K, N, group, sym),), dev)
+    pla = _arg(fn, lora_a, t, (L, r, K), dev)
+    plb = _arg(fn, lora_b, t, (L, N, r), dev)
+    ps = _arg(fn, lora_scale, torch.float32, (L,), dev)
+    pr = _arg(fn, row_adapter, torch.int32, (M,), dev)
+    C = _out(fn, C, t, (M, N), dev)
+    if workspace is None:
+        workspace = _room(fn, None, w4a16_lora_workspace_bytes(M, N, K, group, r, L), dev, zeroed=True)
+    _call(fn, dev, pa, _DTYPES[t], M, K, pw, N, group, int(sym), pla, plb, ps, L, r, pr, C.data_ptr(),
+          _room(fn, workspace, 0, dev).data_ptr(), workspace.numel() * workspace.element_size(),
           _status_arg(fn, dev_status, dev))
     return C
