@@ -439,9 +439,14 @@ W4A16_API int w4a16_moe_combine_grad(const void* dY, const void* Ys, int dtype, 
  *              aligned, under the contract of w4a16_gemm's workspace (first 64 KiB zero before the
  *              first call; calls that share one ordered on the GPU; zeroed again after
  *              W4A16_ETIMEOUT). It may be shared with w4a16_gemm.
- *   kernel     W4A16_KERNEL_AUTO, or a forced W4A16_KERNEL_GEMV or W4A16_KERNEL_TC.
+ *   kernel     W4A16_KERNEL_AUTO (by the mean rows of an expert, R / E), or a forced
+ *              W4A16_KERNEL_GEMV (the decode kernel; R <= max(8, 8 E), else W4A16_EUNSUPPORTED) or
+ *              W4A16_KERNEL_TC.
  *   dev_status device int or NULL: W4A16_ETIMEOUT as for w4a16_gemm.
- *   stream     cudaStream_t. One kernel launch.
+ *   stream     cudaStream_t. Two kernel launches (decode: the activations are laid out first) or one.
+ * Ordering. The decode kernel reads the offsets and weights while its own first kernel still runs,
+ * which in turn lets it start only after everything before the call has completed: no condition
+ * on the kernels before the call.
  * Returns W4A16_OK, W4A16_EINVAL, W4A16_EALIGN, W4A16_EUNSUPPORTED, W4A16_EWORKSPACE or W4A16_ECUDA.
  */
 W4A16_API size_t w4a16_moe_workspace_bytes(int R, int E, int N, int K, int group);

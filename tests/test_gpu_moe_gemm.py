@@ -16,7 +16,7 @@ from weight_only_int4_07_b200 import native, synthetic
 
 pytestmark = pytest.mark.gpu
 TINY = {torch.float16: 2.0 ** -25, torch.bfloat16: 2.0 ** -133}
-KERNELS = [native.KERNEL_AUTO, native.KERNEL_TC]
+KERNELS = [native.KERNEL_AUTO, native.KERNEL_GEMV, native.KERNEL_TC]
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -78,6 +78,9 @@ CASES = [  # counts per expert, K, N, group, sym, dtype: every tile height, empt
     ([0, 1, 0, 1], 256, 256, 128, 0, torch.bfloat16),
     ([2, 0, 1, 3, 0, 0, 9, 1], 1024, 384, 128, 0, torch.float16),
     ([2, 0, 1, 3, 0, 0, 9, 1], 512, 128, 32, 1, torch.bfloat16),
+    ([8, 0, 25, 1, 0, 0, 7, 3, 0, 2], 128, 512, 64, 0, torch.float16),
+    ([0, 0, 16, 0, 0, 0, 0, 20], 384, 1280, 128, 1, torch.float16),
+    ([1] * 40 + [0] * 23 + [17], 256, 128, 128, 0, torch.bfloat16),
     ([17, 1, 40, 0, 16, 2], 512, 256, 64, 0, torch.float16),
     ([33, 1, 100, 0, 16, 2], 384, 256, 32, 0, torch.bfloat16),
     ([0, 150, 64, 65], 640, 384, 128, 1, torch.bfloat16),
@@ -93,6 +96,8 @@ def test_every_run_meets_its_own_weight(counts, K, N, group, sym, dtype, kernel)
     E, off = len(counts), offsets_of(counts)
     n = int(off[E])
     R = n + 3                                          # rows behind the last run: not used
+    if kernel == native.KERNEL_GEMV and R > 8 * max(1, E):
+        pytest.skip("more rows per expert than the decode kernel accepts")
     packed, tiled = experts(E, K, N, group, sym)
     A = activations(R, K, dtype, 3)
     A[n:] = float("nan")

@@ -385,7 +385,7 @@ static int check_moe_gemm(int R, int E, int N, int K, int group) {
 
 W4A16_API size_t w4a16_moe_workspace_bytes(int R, int E, int N, int K, int group) {
     if (check_moe_gemm(R, E, N, K, group) != W4A16_OK) return 0;
-    return kGemvStreamCounterBytes + moe_gemm_partial_bytes(R, E, N, K, group);
+    return kGemvStreamCounterBytes + moe_gemm_partial_bytes(R, E, K);
 }
 
 W4A16_API int w4a16_moe_gemm(const void* A, int a_dtype, int R, int K, const void* tiled, int E,

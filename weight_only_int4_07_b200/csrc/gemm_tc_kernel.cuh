@@ -65,6 +65,7 @@
 
 #include "common.cuh"
 #include "dequant.cuh"
+#include "moe_walk.cuh"
 #include "pdl.cuh"
 #include "sm100_ptx.cuh"
 #include "tiled_layout.cuh"
@@ -142,74 +143,6 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, dev_status, ns));
 }
 
-// kTcGrouped: the runs' table in shared memory, first row, past the last row and first row block of
-// every expert (blocks of BN rows, none for an expert without rows), written by one warp. Offsets
-// outside [0, rows of A] are clamped to it and a run that ends before it begins is empty, so no
-// offset reads or writes outside the buffers.
-__device__ __forceinline__ int2 tc_run(const int32_t* offsets, int e, int M) {
-    const int lo = min(max(__ldg(offsets + e), 0), M), hi = min(max(__ldg(offsets + e + 1), 0), M);
-    return make_int2(lo, max(lo, hi));
-}
-
-__device__ __forceinline__ void tc_group_table(const int32_t* offsets, int E, int M, int bn, int2* run, int* blk) {
-    const int lane = threadIdx.x & 31;
-    int base = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-        const int e = e0 + lane;
-        int2 r = make_int2(0, 0);
-        if (e < E) r = tc_run(offsets, e, M);
-        const int nb = (r.y - r.x + bn - 1) / bn;
-        int x = nb;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, d);
-            if (lane >= d) x += y;
-        }
-        if (e < E) {
-            run[e] = r;
-            blk[e] = base + x - nb;
-        }
-        base += __shfl_sync(0xffffffffu, x, 31);
-    }
-    if (lane == 0) blk[E] = base;
-}
-
-// A role's place among the tiles of a grouped launch, ordered expert-major, then by channel tile,
-// then by row block (the row blocks of one channel tile are neighbours, as in the dense launch).
-struct TcGroupWalk {
-    const int2* run;
-    const int* blk;
-    int e, nt, mb, NT;
-    __device__ __forceinline__ void init(const int2* r, const int* b, int E, int channel_tiles, long long tau) {
-        run = r;
-        blk = b;
-        NT = channel_tiles;
-        int lo = 0, hi = E - 1;   // the last expert whose first tile is at or before tau (one with rows)
-        while (lo < hi) {
-            const int m = (lo + hi + 1) >> 1;
-            if ((long long)blk[m] * NT <= tau) lo = m;
-            else hi = m - 1;
-        }
-        e = lo;
-        const int nb = blk[e + 1] - blk[e];
-        const int q = (int)(tau - (long long)blk[e] * NT);
-        nt = nb > 0 ? q / nb : 0;
-        mb = nb > 0 ? q - nt * nb : 0;
-    }
-    // the next tile (the caller knows that there is one)
-    __device__ __forceinline__ void next() {
-        if (++mb < blk[e + 1] - blk[e]) return;
-        mb = 0;
-        if (++nt < NT) return;
-        nt = 0;
-        do ++e;
-        while (blk[e + 1] == blk[e]);
-    }
-    __device__ __forceinline__ long long rec0(int UT) const { return ((long long)e * NT + nt) * UT; }
-    __device__ __forceinline__ int row0(int bn) const { return run[e].x + mb * bn; }
-    __device__ __forceinline__ int row_end() const { return run[e].y; }
-};
-
 // US (unit-scaled, run at BN = 16 with group 128): every unit's MMAs go to an accumulator of
 // their own, the dequant warps store the exact integers u - z, and the epilogue warps add s times
 // each unit's sums into registers (the unit's scale s of channel n read from its record).
@@ -278,8 +211,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
         // (launched as a programmatic dependent: the rows and offsets may be the previous kernel's)
         pdl_wait();
         pdl_trigger();
-        if (warp == kTcWarpEpi)
-            tc_group_table(p.offsets, p.E, p.M, BN, const_cast<int2*>(run_tab), const_cast<int*>(blk_tab));
+        moe_table(p.offsets, p.E, p.M, BN, const_cast<int2*>(run_tab), const_cast<int*>(blk_tab), [] { cta_sync(); });
     }
     tc_fence_before();
     cta_sync();
@@ -303,7 +235,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
             const long long tau0 = u0 / UT;
             int ku = (int)(u0 - tau0 * UT), mb = kGrp ? 0 : (int)(tau0 % p.mblocks);
             long long nt = kGrp ? 0 : tau0 / p.mblocks;
-            TcGroupWalk gw;
+            MoeWalk gw;
             if constexpr (kGrp) gw.init(run_tab, blk_tab, p.E, p.N / 128, tau0);
             for (long long i = u0; i < u1;) {
                 const int n = UT - ku < kUPL ? (u1 - i < UT - ku ? (int)(u1 - i) : UT - ku)
@@ -344,7 +276,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
             // unit i = tile tau, step ku; row block mb = tau mod mblocks (kept by increments)
             long long tau0 = u0 / UT;
             int ku = (int)(u0 - tau0 * UT), mb = kGrp ? 0 : (int)(tau0 % p.mblocks);
-            TcGroupWalk gw;
+            MoeWalk gw;
             if constexpr (kGrp) gw.init(run_tab, blk_tab, p.E, p.N / 128, tau0);
             for (long long i = u0; i < u1; ++i) {
                 if (i > u0 && ++ku == UT) {
@@ -456,7 +388,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
         T* C = static_cast<T*>(p.C);
         int use[2] = {0, 0}, ab = 0;
         bool ok = true;
-        TcGroupWalk gw;
+        MoeWalk gw;
         if constexpr (kGrp)
             if (u0 < u1) gw.init(run_tab, blk_tab, p.E, p.N / 128, u0 / UT);
         // the counter of a cut tile: one per tile, or (grouped, whose tiles the host cannot count) one

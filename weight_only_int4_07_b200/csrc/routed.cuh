@@ -47,7 +47,10 @@ bool make_act_map(CUtensorMap* map, const void* A, int M, int K, int box_rows, b
 TcPlan plan_tc_rows(int bn, int N, int K, int group, int sym, int ctas, size_t table);
 
 // The experts' products on R sorted rows: workspace after the counters, and the launch.
-size_t moe_gemm_partial_bytes(int R, int E, int N, int K, int group);
+size_t moe_gemm_partial_bytes(int R, int E, int K);
+size_t moe_gemv_partial_bytes(int R, int K);
+int launch_moe_gemv(const void* A, int a_dtype, int R, int K, const void* tiled, int E, const int32_t* offsets, int N,
+                    int group, int sym, void* C, void* workspace, int* dev_status, cudaStream_t stream);
 int launch_moe_gemm(const void* A, int a_dtype, int R, int K, const void* tiled, int E, const int32_t* offsets, int N,
                     int group, int sym, void* C, void* workspace, int kernel, int* dev_status, cudaStream_t stream);
 
