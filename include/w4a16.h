@@ -471,12 +471,14 @@ W4A16_API int w4a16_moe_gemm(const void* A, int a_dtype, int R, int K, const voi
  *   C          device out, [M, N] row-major, dtype a_dtype. Must not overlap an input.
  *   workspace, ws_bytes   device, at least w4a16_lora_workspace_bytes(M, N, K, group, rank, adapters)
  *              bytes, 16-byte aligned, under the contract of w4a16_gemm's workspace. It may be
- *              shared with w4a16_gemm. It holds the FP32 outputs of at most 64 MiB or 256 rows at a
- *              time, whichever is more; longer batches are taken in pieces.
+ *              shared with w4a16_gemm. It holds the rank products of at most 64 MiB or 256 rows at a
+ *              time, whichever is more, and of at most 16384 rows; longer batches are taken in pieces.
  *   dev_status device int or NULL: W4A16_ETIMEOUT as for w4a16_gemm.
- *   stream     cudaStream_t. Three kernel launches up to 16 rows, four above (each piece).
- * The weight buffer must not be written by the kernel that immediately precedes the call (see
- * w4a16_gemm, "Ordering").
+ *   stream     cudaStream_t. Three kernel launches (each piece).
+ * Values that are not finite: those of a row of A, of an adapter or of its scale reach only the rows that
+ * use them (which are then NaN or infinite), never the other rows of the batch.
+ * Ordering. No condition on the kernels before the call (the first kernel lets the layer's start only
+ * after everything before the call has completed).
  * Returns W4A16_OK, W4A16_EINVAL, W4A16_EALIGN, W4A16_EUNSUPPORTED, W4A16_EWORKSPACE or W4A16_ECUDA.
  */
 W4A16_API size_t w4a16_lora_workspace_bytes(int M, int N, int K, int group, int rank, int adapters);

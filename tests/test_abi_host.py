@@ -396,11 +396,12 @@ def test_lora_rejects_bad_arguments_before_any_launch(L):
     mis = P((9 << 20) + 8)
     M, N, K, g, r, n = 4, 256, 512, 128, 16, 8
     need = native.w4a16_lora_workspace_bytes(M, N, K, g, r, n)
-    assert need >= native.w4a16_workspace_bytes(M, N, K, g) + M * N * 4
+    assert need >= 65536 + M * N * 4
     assert native.w4a16_lora_workspace_bytes(M, N, K, g, 12, n) == 0
     assert native.w4a16_lora_workspace_bytes(M, N, K, g, r, 0) == 0
-    # the FP32 outputs of a long batch are held in pieces
+    # the rank products of a long batch are held in pieces
     assert native.w4a16_lora_workspace_bytes(1 << 20, 28672, 4096, g, r, n) < (1 << 28)
+    assert native.w4a16_lora_workspace_bytes(1 << 20, 28672, 4096, g, 256, 1024) < (1 << 28)
 
     def call(A=A, dt=0, M=M, K=K, W=W, N=N, g=g, sym=0, la=la, lb=lb, sc=sc, n=n, r=r, ids=ids, C=C, ws=ws, wsb=need):
         return L.w4a16_lora_gemm(A, dt, M, K, W, N, g, sym, la, lb, sc, n, r, ids, C, ws, wsb, None, None)

@@ -84,6 +84,10 @@ CASES = [  # M, K, N, group, sym, dtype, rank, adapters, ids
     (100, 384, 256, 32, 1, torch.bfloat16, 136, 1024, "any"),
     (257, 512, 384, 128, 0, torch.float16, 64, 3, "runs"),
     (300, 256, 256, 128, 0, torch.bfloat16, 16, 2, "none"),
+    (13, 4096, 256, 128, 0, torch.bfloat16, 48, 13, "any"),       # 16-row tiles, scaled per unit
+    (64, 128, 1280, 32, 0, torch.float16, 16, 64, "any"),         # a weight unit and many low-rank units
+    (130, 256, 2560, 64, 0, torch.bfloat16, 32, 33, "any"),
+    (520, 128, 384, 128, 1, torch.float16, 8, 5, "runs"),
 ]
 
 
@@ -101,12 +105,35 @@ def test_rows_with_their_adapters(M, K, N, group, sym, dtype, r, L, ids):
 
 
 def test_pieces_of_a_long_batch():
-    """More rows than the FP32 outputs are held for: 512 of 28672 channels at a time, then 88."""
-    M, K, N, group, sym, r, L = 600, 128, 28672, 128, 0, 8, 3
+    """More rank products than are held at a time: 256 rows of up to 256 adapters of rank 256, twice,
+    then 88."""
+    M, K, N, group, sym, r, L = 600, 128, 128, 128, 0, 256, 300
     packed, tiled = layer(K, N, group, sym)
-    A, La, Lb, scale, rows = make(M, K, N, r, L, torch.bfloat16, "any")
+    for dtype in (torch.float16, torch.bfloat16):
+        A, La, Lb, scale, rows = make(M, K, N, r, L, dtype, "any")
+        C = native.w4a16_lora_gemm(A.cuda(), tiled, N, group, sym, La.cuda(), Lb.cuda(), scale.cuda(), rows.cuda())
+        check(C, A, La, Lb, scale, rows, packed, N, group, sym)
+
+
+@pytest.mark.parametrize("M", [1, 6, 13, 40, 300])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_an_adapter_that_is_not_finite_stays_with_its_rows(M, dtype):
+    K, N, group, sym, r, L = 1024, 256, 128, 0, 24, 4
+    packed, tiled = layer(K, N, group, sym)
+    A, La, Lb, scale, rows = make(M, K, N, r, L, dtype, torch.arange(M) % (L + 1) - 1)
+    Lb[1, 77, 3] = float("inf")
+    Lb[2, 5, 23] = float("nan")
+    La[3, 1, 9] = float("nan")
     C = native.w4a16_lora_gemm(A.cuda(), tiled, N, group, sym, La.cuda(), Lb.cuda(), scale.cuda(), rows.cuda())
-    check(C, A, La, Lb, scale, rows, packed, N, group, sym, cols=synthetic.column_sample(N, 300, seed=3))
+    good = (rows <= 0).nonzero().view(-1)
+    check(C.cpu()[good], A[good], La, Lb, scale, rows[good], packed, N, group, sym)
+    C = C.cpu()
+    for a, ch in ((1, 77), (2, 5)):
+        mine = (rows == a).nonzero().view(-1)
+        assert not C[mine][:, ch].isfinite().any()
+        others = [n for n in range(N) if n != ch]
+        assert C[mine][:, others].isfinite().all()
+    assert C[rows == 3].isnan().all()
 
 
 @pytest.mark.parametrize("M", [5, 40])

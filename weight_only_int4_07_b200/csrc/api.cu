@@ -320,7 +320,7 @@ static int check_route_rows(int dtype, int H) {
 
 W4A16_API size_t w4a16_moe_sort_workspace_bytes(int T, int k, int E) {
     if (check_route(T, k, E) != W4A16_OK) return 0;
-    return route_sort_workspace_bytes(T, k, E, 0);
+    return route_sort_workspace_bytes(T, k, E);
 }
 
 W4A16_API int w4a16_moe_sort(const int32_t* ids, int T, int k, int E, const void* X, int H, int32_t* offsets,
@@ -333,7 +333,7 @@ W4A16_API int w4a16_moe_sort(const int32_t* ids, int T, int k, int E, const void
     if (!aligned16(ids) || !aligned16(offsets) || !aligned16(rows) || !aligned16(slots) || !aligned16(X) ||
         !aligned16(Xs))
         return W4A16_EALIGN;
-    const size_t need = route_sort_workspace_bytes(T, k, E, 0);
+    const size_t need = route_sort_workspace_bytes(T, k, E);
     if (need > 0 && (!workspace || ws_bytes < need)) return W4A16_EWORKSPACE;
     if (!aligned16(workspace)) return W4A16_EALIGN;
     RouteSort p = {};
@@ -442,14 +442,3 @@ W4A16_API int w4a16_lora_gemm(const void* A, int a_dtype, int M, int K, const vo
 }
 
 }  // extern "C"
-
-int w4a16::launch_gemm_f32(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
-                           float* y, int* slices, void* workspace, int* dev_status, cudaStream_t stream) {
-    if (w4a16_select_kernel(M, N, K, group) == W4A16_KERNEL_GEMV) {
-        const int st = launch_gemv_stream_f32(A, a_dtype, M, K, tiled, N, group, sym, y, slices, workspace, dev_status,
-                                              stream);
-        if (st != W4A16_EUNSUPPORTED) return st;
-    }
-    *slices = 1;
-    return launch_gemm_tc_f32(A, a_dtype, M, K, tiled, N, group, sym, y, workspace, dev_status, stream);
-}

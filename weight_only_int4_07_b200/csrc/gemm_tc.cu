@@ -111,8 +111,8 @@ int launch_gemm_tc(const void* A, int a_dtype, int M, int K, const void* tiled, 
     if (!make_act_map(&map, A, M, K, pl.bn, bf16)) return W4A16_ECUDA;
     TcParams prm = tc_params(pl, tiled, M, N, K, group, sym, bf16, workspace, dev_status);
     prm.C = C;
-    if (bf16) return launch_tc_bn<__nv_bfloat16, kTcDense>(pl.bn, map, prm, pl.smem, stream);
-    return launch_tc_bn<__half, kTcDense>(pl.bn, map, prm, pl.smem, stream);
+    if (bf16) return launch_tc_bn<__nv_bfloat16, kTcDense>(pl.bn, map, map, prm, pl.smem, stream);
+    return launch_tc_bn<__half, kTcDense>(pl.bn, map, map, prm, pl.smem, stream);
 }
 
 }  // namespace w4a16

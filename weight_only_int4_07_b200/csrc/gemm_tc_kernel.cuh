@@ -78,7 +78,7 @@ using namespace sm100;
 
 // What the tiles are and where the sums go.
 constexpr int kTcDense = 0;     // rows [0, M) of A, C in the type of A
-constexpr int kTcF32 = 1;       // the same, FP32 sums to C32 (a later kernel adds to them and rounds)
+constexpr int kTcLora = 1;      // the same, each tile with the low-rank units of its row block (lora.cu)
 constexpr int kTcGrouped = 2;   // runs of rows with a weight of their own each (experts): offsets on the device
 
 constexpr int kTcThreads = 768;
@@ -115,10 +115,15 @@ struct TcParams {
     int* counters;      // one int per tile, zero between calls
     float* partials;    // [P][BN][128]: sums a CTA publishes for the tile that opens its range
     int* dev_status;
-    float* C32;         // kTcF32: [M][N] instead of C
     const int32_t* offsets;   // kTcGrouped: rows offsets[e] .. offsets[e + 1] - 1 meet weight e < E
     int E;
-    uint32_t off_grp;         // kTcGrouped: shared-memory offset of the runs' table
+    uint32_t off_grp;         // kTcGrouped, kTcLora: shared-memory offset of the runs' (units') table
+    const int* lora_units;    // kTcLora: [mblocks] low-rank units of a row block,
+    const int* lora_pieces;   //   [mblocks][max_pieces] 256 a + p: ranks 16 p .. of adapter a, or -1
+    const void* lora_b;       //   [adapters][N][rank]
+    const int32_t* row_adapter;
+    int* lora_bad;            //   set to 1 when some value of a used Lb is not finite
+    int max_pieces, rank, adapters;
     int M, K, N, sym, group;
     uint32_t record, scales_off, zeros_off, slot_w;
     int P, mblocks, nr;
@@ -126,6 +131,10 @@ struct TcParams {
     uint64_t wait_ns;
     GsMasks km;
 };
+
+__device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
 
 __device__ __forceinline__ long long tc_unit_begin(int c, long long U, int P) { return ((long long)c * U) / P; }
 __device__ __forceinline__ int tc_unit_owner(long long u, long long U, int P) {
@@ -143,13 +152,50 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, dev_status, ns));
 }
 
+// kTcLora: a role's place among the units. A tile (channel tile nt, row block mb) has UT = K / 128 weight
+// units, then the row block's low-rank units: 128 K of the products T . Lb^T, where T (bf16, written by
+// lora_place_kernel) holds, for every adapter of the row block, its rows' rank products as hi + lo and
+// zeros in the other rows. cum: low-rank units before each row block.
+struct TcLoraWalk {
+    const int* cum;
+    int UT, mblocks, nt, mb, ku, len;
+    __device__ __forceinline__ void init(const int* c, int units, int blocks, long long u) {
+        cum = c;
+        UT = units;
+        mblocks = blocks;
+        const long long S = (long long)mblocks * UT + cum[mblocks];
+        nt = (int)(u / S);
+        const int r = (int)(u - (long long)nt * S);
+        int lo = 0, hi = mblocks - 1;
+        while (lo < hi) {
+            const int m = (lo + hi + 1) >> 1;
+            if (m * UT + cum[m] <= r) lo = m;
+            else hi = m - 1;
+        }
+        mb = lo;
+        ku = r - (mb * UT + cum[mb]);
+        len = UT + cum[mb + 1] - cum[mb];
+    }
+    // n units further, within the tile or to the start of the next one
+    __device__ __forceinline__ void step(int n) {
+        if ((ku += n) < len) return;
+        ku = 0;
+        if (++mb == mblocks) {
+            mb = 0;
+            ++nt;
+        }
+        len = UT + cum[mb + 1] - cum[mb];
+    }
+    __device__ __forceinline__ bool low() const { return ku >= UT; }
+};
+
 // US (unit-scaled, run at BN = 16 with group 128): every unit's MMAs go to an accumulator of
 // their own, the dequant warps store the exact integers u - z, and the epilogue warps add s times
 // each unit's sums into registers (the unit's scale s of channel n read from its record).
 // Otherwise the dequant warps store (u - z) s and the MMAs accumulate a whole tile segment.
 template <int BN, typename T, bool US, int MODE>
 __global__ void __launch_bounds__(kTcThreads, 1)
-tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
+tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmT, const TcParams p) {
     static_assert(!US || BN <= 32, "unit-scaled accumulation keeps BN sums per thread in registers");
     using Ops = GsOps<T>;
     constexpr int kCols = tc_acc_cols(BN);       // tensor-memory columns of one accumulator
@@ -178,9 +224,11 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int UT = p.K / 128;                              // unit steps per tile
-    constexpr bool kGrp = MODE == kTcGrouped;
+    constexpr bool kGrp = MODE == kTcGrouped, kLora = MODE == kTcLora;
     const int2* run_tab = reinterpret_cast<const int2*>(smem + p.off_grp);   // kTcGrouped
     const int* blk_tab = reinterpret_cast<const int*>(run_tab + p.E);
+    long long* range = reinterpret_cast<long long*>(smem + p.off_grp);       // kTcLora: u0, u1, U, P
+    int* cum_tab = reinterpret_cast<int*>(range + 4);                        // kTcLora
     const int cta = blockIdx.x;
     const uint32_t R = p.record;
     const uint64_t wait_ns = p.wait_ns;
@@ -207,22 +255,48 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
         tmem_alloc(tmem_slot, kTcTmemCols);
         tmem_relinquish();
     }
-    if constexpr (kGrp) {
-        // (launched as a programmatic dependent: the rows and offsets may be the previous kernel's)
+    if constexpr (MODE != kTcDense) {
+        // (launched as a programmatic dependent: what it reads may be the previous kernel's)
         pdl_wait();
         pdl_trigger();
+    }
+    if constexpr (kGrp) {
         moe_table(p.offsets, p.E, p.M, BN, const_cast<int2*>(run_tab), const_cast<int*>(blk_tab), [] { cta_sync(); });
+    }
+    if constexpr (kLora) {
+        if (warp == kTcWarpEpi) {
+            int base = 0;
+            for (int b0 = 0; b0 < p.mblocks; b0 += 32) {
+                const int n = b0 + lane < p.mblocks ? __ldcg(p.lora_units + b0 + lane) : 0;
+                int x = n;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, x, d);
+                    if (lane >= d) x += y;
+                }
+                if (b0 + lane < p.mblocks) cum_tab[b0 + lane] = base + x - n;
+                base += __shfl_sync(0xffffffffu, x, 31);
+            }
+            if (lane == 0) cum_tab[p.mblocks] = base;
+        }
     }
     tc_fence_before();
     cta_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const long long tiles = (long long)(p.N / 128) * (kGrp ? blk_tab[p.E] : p.mblocks);
-    const long long U = tiles * UT;
+    const long long U = tiles * UT + (kLora ? (long long)(p.N / 128) * cum_tab[p.mblocks] : 0);
     // no more ranges than units (the dense launch's host saw to it): none of a tile's ranges is empty
     const int P = kGrp && U < p.P ? (int)U : p.P;
     const bool busy = !kGrp || cta < P;
     const long long u0 = busy ? tc_unit_begin(cta, U, P) : 0, u1 = busy ? tc_unit_begin(cta + 1, U, P) : 0;
+    if constexpr (kLora)
+        if (threadIdx.x == 0) {
+            range[0] = u0;
+            range[1] = u1;
+            range[2] = U;
+            range[3] = P;
+        }
     const uint32_t tmem_w = tmem + (uint32_t)(kBufs * kIss * kCols);   // the step ring's weight tiles
 
     if (warp == kTcWarpLoadW) {
@@ -236,17 +310,30 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
             int ku = (int)(u0 - tau0 * UT), mb = kGrp ? 0 : (int)(tau0 % p.mblocks);
             long long nt = kGrp ? 0 : tau0 / p.mblocks;
             MoeWalk gw;
+            TcLoraWalk lw;
             if constexpr (kGrp) gw.init(run_tab, blk_tab, p.E, p.N / 128, tau0);
+            if constexpr (kLora) lw.init(cum_tab, UT, p.mblocks, u0);
             for (long long i = u0; i < u1;) {
+                if constexpr (kLora) {
+                    if (lw.low()) {   // the dequantizing warps read Lb themselves
+                        const int skip = u1 - i < lw.len - lw.ku ? (int)(u1 - i) : lw.len - lw.ku;
+                        lw.step(skip);
+                        i += skip;
+                        continue;
+                    }
+                    ku = lw.ku;
+                }
                 const int n = UT - ku < kUPL ? (u1 - i < UT - ku ? (int)(u1 - i) : UT - ku)
                                               : (u1 - i < kUPL ? (int)(u1 - i) : kUPL);
                 if (!mbar_wait(&empty_r[rs], rph ^ 1u, abort_flag, p.dev_status, wait_ns)) break;
-                const long long rec = kGrp ? gw.rec0(UT) + ku : nt * UT + ku;
+                const long long rec = (kGrp ? gw.rec0(UT) : (kLora ? (long long)lw.nt : nt) * UT) + ku;
                 mbar_arrive_expect_tx(&full_r[rs], (uint32_t)n * R);
                 bulk_g2s(ring_w + (size_t)rs * p.slot_w, p.tiled + (size_t)rec * R, (uint32_t)n * R, &full_r[rs]);
                 ++issued[rs];
                 i += n;
-                if ((ku += n) == UT) {
+                if constexpr (kLora) {
+                    lw.step(n);
+                } else if ((ku += n) == UT) {
                     ku = 0;
                     if constexpr (kGrp) {
                         if (i < u1) gw.next();
@@ -277,20 +364,27 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
             long long tau0 = u0 / UT;
             int ku = (int)(u0 - tau0 * UT), mb = kGrp ? 0 : (int)(tau0 % p.mblocks);
             MoeWalk gw;
+            TcLoraWalk lw;
             if constexpr (kGrp) gw.init(run_tab, blk_tab, p.E, p.N / 128, tau0);
+            if constexpr (kLora) lw.init(cum_tab, UT, p.mblocks, u0);
             for (long long i = u0; i < u1; ++i) {
-                if (i > u0 && ++ku == UT) {
+                if constexpr (kLora) {
+                    if (i > u0) lw.step(1);
+                } else if (i > u0 && ++ku == UT) {
                     ku = 0;
                     if constexpr (kGrp) gw.next();
                     else if (++mb == p.mblocks) mb = 0;
                 }
                 // (a grouped tile may run into the next expert's rows: those columns are not stored)
-                const int row = kGrp ? gw.row0(BN) : mb * BN;
+                const int row = kGrp ? gw.row0(BN) : (kLora ? lw.mb : mb) * BN;
+                const bool low = kLora && lw.low();
+                const CUtensorMap* map = low ? &tmT : &tmA;
+                const int kx = kLora ? (low ? lw.ku - UT : lw.ku) : ku;
                 if (!mbar_wait(&free_s[s], ph ^ 1u, abort_flag, p.dev_status, wait_ns)) break;
                 mbar_arrive_expect_tx(&full_a[s], kSlotA);
                 uint8_t* dst = ring_a + (size_t)s * kSlotA;
-                tma_2d_g2s(dst, &tmA, ku * 128, row, &full_a[s]);
-                tma_2d_g2s(dst + kSlotA / 2, &tmA, ku * 128 + 64, row, &full_a[s]);
+                tma_2d_g2s(dst, map, kx * 128, row, &full_a[s]);
+                tma_2d_g2s(dst + kSlotA / 2, map, kx * 128 + 64, row, &full_a[s]);
                 ++issued[s];
                 if (++s == NS) {
                     s = 0;
@@ -309,9 +403,12 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
         if (lane == 0) {
             const int j = warp - kTcWarpMma;
             constexpr uint32_t idesc = idesc_f16(BN, std::is_same<T, __nv_bfloat16>::value);
+            constexpr uint32_t idesc_low = idesc_f16(BN, true);   // low-rank units: bf16 on both sides
             int s = 0, use[2] = {0, 0}, ab = 0;
             uint32_t ph = 0;
             bool ok = true;
+            TcLoraWalk lw;
+            if constexpr (kLora) lw.init(cum_tab, UT, p.mblocks, u0);
             if constexpr (US) {
                 // each own unit into accumulator ab * kIss + j (two per issuer, alternating)
                 for (long long i = u0; i < u1; ++i) {
@@ -326,13 +423,15 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
                         const uint32_t d_tmem = tmem + (uint32_t)(slot * kCols);
                         const uint32_t a_tm = tmem_w + (uint32_t)(s * kTcStepCols);
                         const uint32_t b_sm = smem_u32(ring_a + (size_t)s * kSlotA);
-                        mma4_f16_ts(d_tmem, a_tm, smem_desc_sw128(b_sm), idesc, 0u);
-                        mma4_f16_ts(d_tmem, a_tm + 32u, smem_desc_sw128(b_sm + kSlotA / 2), idesc, 1u);
+                        const uint32_t ids = kLora && lw.low() ? idesc_low : idesc;
+                        mma4_f16_ts(d_tmem, a_tm, smem_desc_sw128(b_sm), ids, 0u);
+                        mma4_f16_ts(d_tmem, a_tm + 32u, smem_desc_sw128(b_sm + kSlotA / 2), ids, 1u);
                         mma_commit(&free_s[s]);
                         mma_commit(&accfull[slot]);
                         ++use[ab];
                         ab ^= 1;
                     }
+                    if constexpr (kLora) lw.step(1);
                     if (++s == NS) {
                         s = 0;
                         ph ^= 1u;
@@ -341,8 +440,9 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
                 ok = false;   // (the tile loop below is not run)
             }
             for (long long i = u0; i < u1 && ok;) {
-                const long long tau = i / UT;
-                const long long seg_end = u1 < (tau + 1) * UT ? u1 : (tau + 1) * UT;
+                const long long tau = kLora ? 0 : i / UT;
+                const long long tile_end = kLora ? i + (lw.len - lw.ku) : (tau + 1) * UT;
+                const long long seg_end = u1 < tile_end ? u1 : tile_end;
                 if (!mbar_wait(&accempty[ab], ((uint32_t)use[ab] & 1u) ^ 1u, abort_flag, p.dev_status, wait_ns)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem + (uint32_t)((ab * kIss + j) * kCols);
@@ -359,11 +459,13 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
                         // from the two 64-K boxes of the step's tile; one commit frees both tiles
                         const uint32_t a_tm = tmem_w + (uint32_t)(s * kTcStepCols);
                         const uint32_t b_sm = smem_u32(ring_a + (size_t)s * kSlotA);
-                        mma4_f16_ts(d_tmem, a_tm, smem_desc_sw128(b_sm), idesc, first ? 0u : 1u);
-                        mma4_f16_ts(d_tmem, a_tm + 32u, smem_desc_sw128(b_sm + kSlotA / 2), idesc, 1u);
+                        const uint32_t ids = kLora && lw.low() ? idesc_low : idesc;
+                        mma4_f16_ts(d_tmem, a_tm, smem_desc_sw128(b_sm), ids, first ? 0u : 1u);
+                        mma4_f16_ts(d_tmem, a_tm + 32u, smem_desc_sw128(b_sm + kSlotA / 2), ids, 1u);
                         mma_commit(&free_s[s]);
                         first = false;
                     }
+                    if constexpr (kLora) lw.step(1);
                     if (++s == NS) {
                         s = 0;
                         ph ^= 1u;
@@ -391,12 +493,27 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
         MoeWalk gw;
         if constexpr (kGrp)
             if (u0 < u1) gw.init(run_tab, blk_tab, p.E, p.N / 128, u0 / UT);
-        // the counter of a cut tile: one per tile, or (grouped, whose tiles the host cannot count) one
-        // per CTA, of the one cut tile that the CTA opens
-        auto counter = [&](long long tau, int cf) { return p.counters + (kGrp ? (long long)cf : tau); };
-        auto put = [&](size_t at, float y) {
-            if constexpr (MODE == kTcF32) p.C32[at] = y;
-            else C[at] = Act<T>::from_f32(y);
+        TcLoraWalk lw;
+        if constexpr (kLora) lw.init(cum_tab, UT, p.mblocks, u0);
+        // the counter of a cut tile: one per tile (dense), or one per CTA, of the one cut tile that
+        // opens in the CTA's range
+        auto counter = [&](long long tau, int cf) { return p.counters + (MODE == kTcDense ? tau : (long long)cf); };
+        auto put = [&](size_t at, float y) { C[at] = Act<T>::from_f32(y); };
+        // kTcLora: the tile's rows of every Lb it takes, on their way to L2 while the weight units run (a
+        // fetch by the dequantizing warps that finds them in HBM waits behind the weight stream: 3.6 us
+        // per low-rank unit at 16 rows of 14 adapters)
+        auto ahead = [&](int tile_nt, int mb, int low_units) {
+            if constexpr (kLora) {
+                constexpr int kPer = std::is_same<T, __nv_bfloat16>::value ? 4 : 2;
+                const int pr = (p.rank + 15) / 16;
+                for (int j = n; j * pr < low_units * kPer; j += 128) {
+                    const int piece = __ldg(p.lora_pieces + (size_t)mb * p.max_pieces + j * pr);
+                    if (piece >= 0)
+                        bulk_prefetch_l2(static_cast<const T*>(p.lora_b) +
+                                             ((size_t)(piece >> 8) * p.N + (size_t)tile_nt * 128) * p.rank,
+                                         256u * (uint32_t)p.rank);
+                }
+            }
         };
         if constexpr (US) {
             // per unit: s times the unit's sums into run[] (row m0 + r of channel n); per tile
@@ -409,20 +526,24 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
             for (int k = 0; k < 2 * kIss; ++k) uses[k] = 0;
             const uint16_t* scl = reinterpret_cast<const uint16_t*>(p.tiled + p.scales_off) + n;
             for (long long i = u0; i < u1;) {
-                const long long tau = i / UT;
-                const long long seg_end = u1 < (tau + 1) * UT ? u1 : (tau + 1) * UT;
+                const long long tau = kLora ? 0 : i / UT;
+                const long long t0u = kLora ? i - lw.ku : tau * UT, t1u = t0u + (kLora ? lw.len : UT);   // the tile's units
+                const long long seg_end = u1 < t1u ? u1 : t1u;
                 if constexpr (kGrp)
                     if (i > u0) gw.next();
-                const int nt = kGrp ? gw.nt : (int)(tau / p.mblocks), mb = kGrp ? 0 : (int)(tau % p.mblocks);
+                const int nt = kGrp ? gw.nt : kLora ? lw.nt : (int)(tau / p.mblocks);
+                const int mb = kGrp ? 0 : kLora ? lw.mb : (int)(tau % p.mblocks);
                 const size_t n0 = (size_t)nt * 128;
                 const int m0 = kGrp ? gw.row0(BN) : mb * BN, mend = kGrp ? gw.row_end() : p.M;
-                const int cf = tc_unit_owner(tau * UT, U, P), cl = tc_unit_owner(tau * UT + UT - 1, U, P);
+                const int cf = tc_unit_owner(t0u, U, P), cl = tc_unit_owner(t1u - 1, U, P);
+                if (kLora && seg_end > t0u + UT) ahead(nt, mb, lw.len - UT);
                 for (; i < seg_end; ++i) {
                     const int j = kIss == 1 ? 0 : (int)((i - u0) & 1);
                     const int slot = abj[j] * kIss + j;
                     // the unit's record is nt K/128 + its K-step; its scale of channel n (group 128)
-                    const long long rec = (kGrp ? gw.rec0(UT) : (long long)nt * UT) + (i - tau * UT);
-                    const uint16_t sb = __ldg(scl + (size_t)rec * (R / 2));
+                    const long long rec = (kGrp ? gw.rec0(UT) : (long long)nt * UT) + (i - t0u);
+                    // (a low-rank unit's sums count as they are: 1 in fp16)
+                    const uint16_t sb = kLora && lw.low() ? (uint16_t)0x3C00u : __ldg(scl + (size_t)rec * (R / 2));
                     ok = ok && tc_wait(&accfull[slot], (uint32_t)uses[slot] & 1u, abort_flag, p.dev_status, wait_ns);
                     tc_fence_after();
                     if (ok) {
@@ -442,6 +563,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
                     if (lane == 0) mbar_arrive(&accempty[slot]);
                     ++uses[slot];
                     abj[j] ^= 1;
+                    if constexpr (kLora) lw.step(1);
                 }
                 if (cf == cl || cta == cf) {
                     if (cf != cl) {
@@ -502,8 +624,10 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
             ok = false;   // (the tile loop below is not run)
         }
         for (long long i = u0; i < u1 && (!US || ok);) {
-            const long long tau = i / UT;
-            const long long seg_end = u1 < (tau + 1) * UT ? u1 : (tau + 1) * UT;
+            const long long tau = kLora ? 0 : i / UT;
+            const long long t0u = kLora ? i - lw.ku : tau * UT, t1u = t0u + (kLora ? lw.len : UT);   // the tile's units
+            const long long seg_end = u1 < t1u ? u1 : t1u;
+            if (kLora && seg_end > t0u + UT) ahead(lw.nt, lw.mb, lw.len - UT);
             // the issuers that hold units of this tile segment (issuer j: units j, j + 2, ..)
             const long long seg_lo = i;
             const bool has0 = kIss == 1 || seg_end - seg_lo >= 2 || ((seg_lo - u0) & 1) == 0;
@@ -512,10 +636,12 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
             tc_fence_after();
             if constexpr (kGrp)
                 if (i > u0) gw.next();
-            const int nt = kGrp ? gw.nt : (int)(tau / p.mblocks), mb = kGrp ? 0 : (int)(tau % p.mblocks);
+            const int nt = kGrp ? gw.nt : kLora ? lw.nt : (int)(tau / p.mblocks);
+            const int mb = kGrp ? 0 : kLora ? lw.mb : (int)(tau % p.mblocks);
             const size_t n0 = (size_t)nt * 128;
             const int m0 = kGrp ? gw.row0(BN) : mb * BN, mend = kGrp ? gw.row_end() : p.M;
-            const int cf = tc_unit_owner(tau * UT, U, P), cl = tc_unit_owner(tau * UT + UT - 1, U, P);
+            const int cf = tc_unit_owner(t0u, U, P), cl = tc_unit_owner(t1u - 1, U, P);
+            if constexpr (kLora) lw.step((int)(seg_end - i));
             i = seg_end;
             const uint32_t lane_base = tmem + (uint32_t)(ab * kIss * kCols) + ((uint32_t)(32 * q) << 16);
             // the tile's FP32 sums, 16 columns from c: the issuers' accumulators added
@@ -623,11 +749,114 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
         uint32_t rph = 0, ph = 0;
         bool ok = true;
         long long tend = (u0 / UT + 1) * UT;   // end of the current tile's units
+        // kTcLora: block blk's 16 ranks of Lb, fetched a unit ahead, and the piece after them
+        [[maybe_unused]] TcLoraWalk lw;
+        [[maybe_unused]] uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
+        [[maybe_unused]] int piece = -1;
+        auto piece_of = [&](int unit) {   // low-rank unit of the walk's row block
+            constexpr int kPer = std::is_same<T, __nv_bfloat16>::value ? 4 : 2;   // pieces per unit
+            return __ldg(p.lora_pieces + (size_t)lw.mb * p.max_pieces + unit * kPer + (kPer == 4 ? blk : blk >> 1));
+        };
+        auto fetch = [&]() {
+            b0 = b1 = make_uint4(0, 0, 0, 0);
+            if (piece < 0) return;
+            const int j = 16 * (piece & 255);
+            const uint4* src = reinterpret_cast<const uint4*>(
+                static_cast<const T*>(p.lora_b) + ((size_t)(piece >> 8) * p.N + (size_t)lw.nt * 128 + n) * p.rank + j);
+            b0 = __ldg(src);
+            if (j + 8 < p.rank) b1 = __ldg(src + 1);
+        };
+        if constexpr (kLora) {
+            lw.init(cum_tab, UT, p.mblocks, u0);
+            if (u0 < u1 && lw.len > UT) {
+                piece = piece_of(lw.low() ? lw.ku - UT : 0);
+                if (lw.low()) {
+                    fetch();
+                    if (lw.ku + 1 < lw.len) piece = piece_of(lw.ku + 1 - UT);
+                }
+            }
+        }
         for (long long i = u0; i < u1 && ok;) {
+            if constexpr (kLora) {
+                if (lw.low()) {
+                    // bf16 layer: [Lb | Lb] beside T's [hi | lo]; fp16 layer: Lb = hi + lo exactly (8 + 3
+                    // bits), blocks [hi | hi], [lo | 0] beside T's [hi | lo], [hi | 0]
+                    if (!tc_wait(&free_s[s], ph ^ 1u, abort_flag, p.dev_status, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    uint32_t w8[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+                    uint32_t out[16];
+                    {
+                        constexpr uint32_t kExp = std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u;
+                        bool bad = false;
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const bool bl = (w8[c] & kExp) == kExp, bh = (w8[c] & (kExp << 16)) == (kExp << 16);
+                            w8[c] &= (bl ? 0u : 0xFFFFu) | (bh ? 0u : 0xFFFF0000u);
+                            bad = bad || bl || bh;
+                        }
+                        if (bad) {
+                            *static_cast<volatile int*>(p.lora_bad) = 1;
+                            __threadfence();
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                            out[c] = out[8 + c] = w8[c];
+                        } else {
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w8[c]));
+                            const uint32_t hx = __float_as_uint(f.x) & 0xFFFF0000u, hy = __float_as_uint(f.y) & 0xFFFF0000u;
+                            const uint32_t lx = __float_as_uint(f.x - __uint_as_float(hx));
+                            const uint32_t ly = __float_as_uint(f.y - __uint_as_float(hy));
+                            const uint32_t hi = (hx >> 16) | hy, lo = (lx >> 16) | (ly & 0xFFFF0000u);
+                            out[c] = blk & 1 ? lo : hi;
+                            out[8 + c] = blk & 1 ? 0u : hi;
+                        }
+                    }
+                    lw.step(1);
+                    ++i;
+                    if (i < u1 && lw.len > UT) {
+                        if (lw.low()) {
+                            fetch();
+                            if (lw.ku + 1 < lw.len) piece = piece_of(lw.ku + 1 - UT);
+                        } else {
+                            piece = piece_of(0);
+                        }
+                    }
+                    tmem_st16(d_lane + (uint32_t)(s * kTcStepCols), out);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&full_d[s]);
+                    if (++s == NS) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                    continue;
+                }
+                tend = i + (UT - lw.ku);
+            }
             const long long seg_end = u1 < tend ? u1 : tend;
             const int nu = (int)(seg_end - i < kUPL ? seg_end - i : kUPL);
             i += nu;
-            if (i == tend) tend += UT;
+            if constexpr (kLora) {
+                const bool last = lw.ku + nu == UT && lw.len > UT;   // the low-rank units come next
+                lw.ku += nu;
+                if (last) {
+                    fetch();
+                    if (lw.len > UT + 1) piece = piece_of(1);
+                }
+                if (lw.ku == lw.len) {
+                    lw.ku -= nu;
+                    lw.step(nu);
+                    if (i < u1 && lw.len > UT) piece = piece_of(0);
+                }
+            } else if (i == tend) {
+                tend += UT;
+            }
             if (!tc_wait(&full_r[rs], rph, abort_flag, p.dev_status, wait_ns)) {
                 ok = false;
                 break;
@@ -684,6 +913,37 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const TcParams p) {
 
     tc_fence_before();
     cta_sync();
+    if constexpr (kLora) {
+        // Values of Lb that are not finite entered the products as 0, or they would have reached the other
+        // rows of the block (0 times them); the rows of their adapter get NaN here. Seldom run, and kept
+        // out of the epilogue's loop, where its mere presence cost 5 us per tile. (The flag is seen:
+        // it was set before the unit's weights were handed over, here or by the CTAs of a cut tile.)
+        if (*static_cast<volatile int*>(p.lora_bad) != 0) {
+            // (from shared memory: kept in registers since the start they spilled the roles' loops)
+            const volatile long long* rg = range;
+            const long long U_ = rg[2], u1_ = rg[1];
+            const int P_ = (int)rg[3];
+            TcLoraWalk lw;
+            lw.init(cum_tab, p.K / 128, p.mblocks, rg[0]);
+            for (long long i = rg[0]; i < u1_;) {
+                const long long t1u = i - lw.ku + lw.len;
+                const int m0 = lw.mb * BN, rows = p.M - m0 < BN ? p.M - m0 : BN;
+                if (tc_unit_owner(i - lw.ku, U_, P_) == (int)blockIdx.x)
+                    for (int o = threadIdx.x; o < rows * 128; o += kTcThreads) {
+                        const int m = m0 + (o >> 7), a = p.row_adapter[m];
+                        const size_t ch = (size_t)lw.nt * 128 + (o & 127);
+                        if ((unsigned)a >= (unsigned)p.adapters) continue;
+                        const T* b = static_cast<const T*>(p.lora_b) + ((size_t)a * p.N + ch) * p.rank;
+                        bool bad = false;
+                        for (int j = 0; j < p.rank; ++j) bad = bad || !isfinite(Act<T>::to_f32(b[j]));
+                        if (bad) static_cast<T*>(p.C)[(size_t)m * p.N + ch] = Act<T>::from_f32(__int_as_float(0x7FC00000));
+                    }
+                const long long to = u1_ < t1u ? u1_ : t1u;
+                lw.step((int)(to - i));
+                i = to;
+            }
+        }
+    }
     if (warp == kTcWarpLoadA) {
         tc_fence_after();
         tmem_dealloc(tmem, kTcTmemCols);
@@ -728,7 +988,7 @@ inline TcParams tc_params(const TcPlan& pl, const void* tiled, int M, int N, int
 }
 
 template <int BN, typename T, bool US, int MODE>
-int launch_tc_typed(const CUtensorMap& map, const TcParams& prm, size_t smem, cudaStream_t stream) {
+int launch_tc_typed(const CUtensorMap& map, const CUtensorMap& map_t, const TcParams& prm, size_t smem, cudaStream_t stream) {
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [] {
@@ -736,26 +996,26 @@ int launch_tc_typed(const CUtensorMap& map, const TcParams& prm, size_t smem, cu
                                         kTcSmemMax);
     });
     if (attr_err != cudaSuccess) return W4A16_ECUDA;
-    if constexpr (MODE == kTcGrouped)
-        return launch_pdl(tc_gemm_kernel<BN, T, US, MODE>, dim3(prm.P), dim3(kTcThreads), smem, stream, map, prm) ==
+    if constexpr (MODE != kTcDense)
+        return launch_pdl(tc_gemm_kernel<BN, T, US, MODE>, dim3(prm.P), dim3(kTcThreads), smem, stream, map, map_t, prm) ==
                        cudaSuccess
                    ? W4A16_OK
                    : W4A16_ECUDA;
-    tc_gemm_kernel<BN, T, US, MODE><<<prm.P, kTcThreads, smem, stream>>>(map, prm);
+    tc_gemm_kernel<BN, T, US, MODE><<<prm.P, kTcThreads, smem, stream>>>(map, map_t, prm);
     return launch_status();
 }
 
 template <typename T, int MODE>
-int launch_tc_bn(int bn, const CUtensorMap& map, const TcParams& prm, size_t smem, cudaStream_t stream) {
+int launch_tc_bn(int bn, const CUtensorMap& map, const CUtensorMap& map_t, const TcParams& prm, size_t smem, cudaStream_t stream) {
     switch (bn) {
         // unit-scaled accumulation where one group spans a unit, at BN = 16 (measured on the
         // (8192, 28672) layer: 71.2 -> 67.8 us at M = 16; at BN = 32 it was slower, 74.4 -> 76.6)
-        case 16: return prm.group == 128 ? launch_tc_typed<16, T, true, MODE>(map, prm, smem, stream)
-                                         : launch_tc_typed<16, T, false, MODE>(map, prm, smem, stream);
-        case 32: return launch_tc_typed<32, T, false, MODE>(map, prm, smem, stream);
-        case 64: return launch_tc_typed<64, T, false, MODE>(map, prm, smem, stream);
-        case 128: return launch_tc_typed<128, T, false, MODE>(map, prm, smem, stream);
-        case 256: return launch_tc_typed<256, T, false, MODE>(map, prm, smem, stream);
+        case 16: return prm.group == 128 ? launch_tc_typed<16, T, true, MODE>(map, map_t, prm, smem, stream)
+                                         : launch_tc_typed<16, T, false, MODE>(map, map_t, prm, smem, stream);
+        case 32: return launch_tc_typed<32, T, false, MODE>(map, map_t, prm, smem, stream);
+        case 64: return launch_tc_typed<64, T, false, MODE>(map, map_t, prm, smem, stream);
+        case 128: return launch_tc_typed<128, T, false, MODE>(map, map_t, prm, smem, stream);
+        case 256: return launch_tc_typed<256, T, false, MODE>(map, map_t, prm, smem, stream);
         default: return W4A16_EUNSUPPORTED;
     }
 }

@@ -1,31 +1,35 @@
 // lora.cu -- low-rank adapters of many requests at once beside the INT4 layer (sm_100a).
 //
 // C[m] = A[m] . dequant(W) + s_a (A[m] . La_a^T) . Lb_a^T,  a = row m's adapter (none: the first term).
-// Three kernels after one another, joined by programmatic dependent launch:
-//   shrink  T[m, j] = sum_k A[m, k] La_a[j, k] over slices of K (FP32 partial sums per slice);
-//   base    the layer's own kernel with FP32 output (gemv_stream.cu or gemm_tc_kernel.cuh);
-//   expand  C = base + 2^e (T 2^-e s_a) . Lb_a^T, rounded once.
-// Rows of one adapter are taken together, so an adapter's matrices come from memory once however many
-// requests use it: up to 16 rows each CTA groups them itself, above a counting sort (moe_route.cu)
-// lists runs of up to 32 rows.
-// Both products are m16n8k16 warp MMAs on operands read straight from global memory: a lane reads 16
-// (or 8) consecutive bytes of a row and the same permutation of K (or of the ranks) stands on both
-// sides of the product, so no shared-memory staging is needed. The work is small beside the
-// layer's (2 r (K + N) of 2 K N operations per row); what counts is that it streams at full width.
-// T stays at FP32 accuracy: it enters the second product as the sum of two 16-bit values, hi and lo,
-// after a power of two per row that puts its largest value near 2^14 (fp16 then keeps everything
-// down to 2^-38 of it).
+//   shrink  T[m, j] = s_a sum_k A[m, k] La_a[j, k], FP32 partial sums over slices of K. Both operands of
+//           its warp MMAs (m16n8k16) come straight from global memory: a lane reads 16 consecutive
+//           bytes of a row and the same permutation of K stands on both sides. Rows of one adapter
+//           within a block of 16 or 32 rows are taken together.
+// Then, where the layer runs on the tensor cores (launch_lora_tc):
+//   place   per block of BN rows, T as a matrix with one run of columns per adapter of the block, its
+//           rows' values there (as bf16 hi + lo) and zeros in the other rows;
+//   layer   the tensor-core GEMM (kTcLora), whose tiles go on over those columns: the second product is
+//           a few more steps of the same accumulation. One rounding, no intermediate of C's size. (A
+//           kernel that added T . Lb^T to FP32 outputs of the layer took 93 us of every 512 rows
+//           of the 4096 x 28672 layer, beside the layer's 117.)
+// and for few rows, where the decode kernel streams the layer (launch_lora_gemv):
+//   layer   that kernel with FP32 outputs;
+//   expand  C = outputs + 2^e (T 2^-e) . Lb_a^T, rounded once, again on warp MMAs from global memory: T
+//           enters as hi + lo in 16 bits under a power of two per row that puts its largest value near
+//           2^14 (fp16 then keeps everything down to 2^-38 of it).
+// The kernels follow each other by programmatic dependent launch.
+#include <type_traits>
+
+#include "gemm_tc_kernel.cuh"
 #include "pdl.cuh"
-#include "dequant.cuh"
 #include "routed.cuh"
 
 namespace w4a16 {
 namespace {
 
 constexpr int kLoraThreads = 256, kLoraWarps = kLoraThreads / 32;
-constexpr int kLoraSmallRows = 16;          // up to here CTAs group the rows themselves
-constexpr int kShrinkRanks = 64;            // ranks of one pass over K
-constexpr size_t kLoraChunkBytes = (size_t)64 << 20;   // FP32 base outputs held at a time
+constexpr size_t kLoraPlaceBytes = (size_t)64 << 20;   // T as placed, held at a time (or 256 rows of it)
+constexpr int kLoraMaxChunk = 16384;
 
 struct LoraParams {
     const void* A;              // [M, K]
@@ -33,55 +37,50 @@ struct LoraParams {
     const void* Lb;             // [L, N, r]
     const float* scale;         // [L]
     const int32_t* row_adapter; // [M]
-    const RouteTile* tiles;     // M > 16: runs of sorted rows
-    const int* ntiles;
-    const int32_t* rows;        // sorted row -> row
     float* part;                // [S][M][r]
     const float* base;          // [slices][M][N]
     void* C;
-    int M, K, N, r, L, S, slices, passes;
+    int M, K, N, r, L, S, slices;
 };
 
-// The rows of one work item: those of tile `i`, or (up to 16 rows) the rows that share row i's
-// adapter when i is the first of them. `list` (shared) gets their indices; returns how many, 0 for
-// none. All threads of the CTA call it.
-__device__ __forceinline__ int lora_rows(const LoraParams& p, int i, int* list, int& adapter) {
-    if (p.tiles) {
-        if (i >= *p.ntiles) return 0;
-        const RouteTile t = p.tiles[i];
-        adapter = t.bin;
-        if (threadIdx.x < t.count) list[threadIdx.x] = p.rows[t.begin + threadIdx.x];
-        __syncthreads();
-        return t.count;
+// Row `lane` of a block of up to 32 rows from row m0: its adapter (-1: none), the lanes that share it,
+// and one bit per adapter of the block, at its first row.
+struct LoraBlock {
+    int adapter;
+    unsigned peers, firsts;
+    __device__ __forceinline__ LoraBlock(const LoraParams& p, int m0, int rows) {
+        const int lane = threadIdx.x & 31;
+        adapter = lane < rows && m0 + lane < p.M ? p.row_adapter[m0 + lane] : -1;
+        if ((unsigned)adapter >= (unsigned)p.L) adapter = -1;
+        peers = __match_any_sync(0xffffffffu, adapter);
+        firsts = __ballot_sync(0xffffffffu, adapter >= 0 && __ffs(peers) - 1 == lane);
     }
-    const int lane = threadIdx.x & 31;
-    int a = -1;
-    if (lane < p.M) {
-        a = p.row_adapter[lane];
-        if ((unsigned)a >= (unsigned)p.L) a = p.L;
-    }
-    adapter = __shfl_sync(0xffffffffu, a, i);
-    const unsigned same = __ballot_sync(0xffffffffu, lane < p.M && a == adapter);
-    if (__ffs(same) - 1 != i) return 0;
-    if (threadIdx.x < 32 && (same >> lane) & 1u) list[__popc(same & ((1u << lane) - 1u))] = lane;
-    __syncthreads();
-    return __popc(same);
-}
+};
 
-// T's partial sums over one slice of K. NB: 8-row blocks (2: up to 16 rows, 4: up to 32). Warp w takes
-// every eighth 32-K step of the slice; MMA rows are ranks, MMA columns rows of A.
-template <int NB, typename T>
-__global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const LoraParams p) {
-    constexpr int RB = kShrinkRanks / 16;
-    __shared__ float red[4][kShrinkRanks * NB * 8];
+// T's partial sums over one slice of K (blockIdx.x) for a block of 8 NB rows (blockIdx.y); the adapters
+// of the block are dealt out to gridDim.z CTAs. Warp w takes every eighth 32-K step of the slice; MMA
+// rows are ranks, MMA columns the adapter's rows.
+// RB: 16-rank blocks of one pass over K.
+template <int NB, int RB, typename T>
+__global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const LoraParams p) {
+    __shared__ float red[4][RB * NB * 128];
     __shared__ int list[32];
     using Ops = GsOps<T>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     pdl_wait();
     pdl_trigger();
-    int adapter;
-    const int n = lora_rows(p, blockIdx.y, list, adapter);
-    if (n == 0 || adapter >= p.L) return;
+    const LoraBlock blk(p, blockIdx.y * 8 * NB, 8 * NB);
+    const int here = __popc(blk.firsts);
+    for (int nth = blockIdx.z; nth < here; nth += gridDim.z) {
+    unsigned left = blk.firsts;
+    for (int q = 0; q < nth; ++q) left &= left - 1;
+    const int first = __ffs(left) - 1;
+    const int adapter = __shfl_sync(0xffffffffu, blk.adapter, first);
+    const unsigned same = __shfl_sync(0xffffffffu, blk.peers, first);
+    const int n = __popc(same);
+    __syncthreads();   // (the last adapter's rows have been used)
+    if (threadIdx.x < 32 && ((same >> lane) & 1u)) list[__popc(same & ((1u << lane) - 1u))] = blockIdx.y * 8 * NB + lane;
+    __syncthreads();
     const T* A = static_cast<const T*>(p.A);
     const T* La = static_cast<const T*>(p.La) + (size_t)adapter * p.r * p.K;
     const int steps = p.K / 32, S = p.S, sl = blockIdx.x;
@@ -89,14 +88,14 @@ __global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const LoraPar
     const T* x[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) x[b] = 8 * b + g < n ? A + (size_t)list[8 * b + g] * p.K + 8 * t : nullptr;
-    for (int r0 = 0; r0 < p.r; r0 += kShrinkRanks) {
+    for (int r0 = 0; r0 < p.r; r0 += 16 * RB) {
         float acc[RB][NB][4];
 #pragma unroll
         for (int q = 0; q < RB; ++q)
 #pragma unroll
             for (int b = 0; b < NB; ++b) acc[q][b][0] = acc[q][b][1] = acc[q][b][2] = acc[q][b][3] = 0.0f;
         const int nq = min(RB, (p.r - r0 + 15) / 16);
-#pragma unroll 2
+#pragma unroll(RB == 1 ? 4 : RB == 2 ? 2 : 1)
         for (int s = s0 + warp; s < s1; s += kLoraWarps) {
             uint4 xv[NB], lo[RB], hi[RB];
             const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -115,38 +114,34 @@ __global__ void __launch_bounds__(kLoraThreads) lora_shrink_kernel(const LoraPar
                 if (q < nq)
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
+                        if (8 * b >= n) break;   // no row of the adapter in this block of columns
                         Ops::mma(acc[q][b], lo[q].x, hi[q].x, lo[q].y, hi[q].y, xv[b].x, xv[b].y);
                         Ops::mma(acc[q][b], lo[q].z, hi[q].z, lo[q].w, hi[q].w, xv[b].z, xv[b].w);
                     }
         }
-        // the warps' sums, halves onto halves (a fixed order)
+        // the warps' sums in a fixed order: 4..7 onto 0..3 through shared memory, then one thread per
+        // output adds the four
         auto each = [&](auto f) {
 #pragma unroll
             for (int q = 0; q < RB; ++q)
 #pragma unroll
                 for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) f(acc[q][b][e], ((q * NB + b) * 4 + e) * 32 + lane);
+                    for (int e = 0; e < 4; ++e)
+                        if (q < nq && 8 * b < n) f(acc[q][b][e], ((q * NB + b) * 4 + e) * 32 + lane);
         };
-#pragma unroll
-        for (int half = kLoraWarps / 2; half >= 1; half >>= 1) {
-            if (warp >= half && warp < 2 * half) each([&](float& v, int at) { red[warp - half][at] = v; });
-            __syncthreads();
-            if (warp < half) each([&](float& v, int at) { v += red[warp][at]; });
-            __syncthreads();
+        if (warp >= 4) each([&](float& v, int at) { red[warp - 4][at] = v; });
+        __syncthreads();
+        if (warp < 4) each([&](float& v, int at) { red[warp][at] += v; });
+        __syncthreads();
+        float* out = p.part + (size_t)sl * p.M * p.r;
+        for (int o = threadIdx.x; o < n * RB * 16; o += kLoraThreads) {
+            const int m = o / (RB * 16), j = o % (RB * 16);   // the adapter's row m, rank r0 + j
+            const int at = (((j >> 4) * NB + (m >> 3)) * 4 + (m & 1) + ((j >> 2) & 2)) * 32 + (j & 7) * 4 + ((m & 7) >> 1);
+            if (r0 + j < p.r) out[(size_t)list[m] * p.r + r0 + j] = (red[0][at] + red[1][at]) + (red[2][at] + red[3][at]);
         }
-        if (warp == 0) {
-            float* out = p.part + (size_t)sl * p.M * p.r;
-#pragma unroll
-            for (int q = 0; q < RB; ++q)
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = r0 + 16 * q + g + 8 * (e >> 1), m = 8 * b + 2 * t + (e & 1);
-                        if (j < p.r && m < n) out[(size_t)list[m] * p.r + j] = acc[q][b][e];
-                    }
-        }
+        __syncthreads();
+    }
     }
 }
 
@@ -155,29 +150,35 @@ __host__ __device__ inline int lora_t_stride(int r) {   // elements between rows
     return (bytes % 64 == 0 ? bytes + 32 : bytes) / 2;    // 32 mod 64: the lanes' 8-byte reads miss no bank
 }
 
-// C's rows of one item and `passes` blocks of 256 channels. NB: 16-row blocks. MMA rows are rows of C,
-// MMA columns channels: column c of tile j is channel 8 (c / 2) + 2 j + c % 2 of the warp's 32, so a
-// lane's four tiles are eight consecutive channels of C.
-template <int NB, typename T>
+// The second product of up to 16 rows: blockIdx.y is a row, the CTA takes all rows that share its
+// adapter when it is the first of them, and 256 channels. MMA rows are rows of C, MMA columns channels:
+// column c of tile j is channel 8 (c / 2) + 2 j + c % 2 of the warp's 32, so a lane's four tiles are
+// eight consecutive channels of C.
+template <typename T>
 __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraParams p) {
     extern __shared__ __align__(16) uint8_t lora_smem[];
-    __shared__ int list[32];
-    __shared__ float up[16 * NB];
+    __shared__ int list[16];
+    __shared__ float up[16];
     using Ops = GsOps<T>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int ts = lora_t_stride(p.r), r16 = (p.r + 15) / 16;
     T* thi = reinterpret_cast<T*>(lora_smem);
-    T* tlo = thi + (size_t)16 * NB * ts;
+    T* tlo = thi + (size_t)16 * ts;
     pdl_wait();
     pdl_trigger();
-    int adapter;
-    const int n = lora_rows(p, blockIdx.y, list, adapter);
-    if (n == 0) return;
-    const bool low = adapter < p.L;
+    const LoraBlock blk(p, 0, 16);
+    const int i = blockIdx.y;
+    const int adapter = __shfl_sync(0xffffffffu, blk.adapter, i);
+    const unsigned same = __shfl_sync(0xffffffffu, blk.peers, i) & ((1u << p.M) - 1u);
+    if (__ffs(same) - 1 != i) return;
+    const int n = __popc(same);
+    if (threadIdx.x < 32 && ((same >> lane) & 1u)) list[__popc(same & ((1u << lane) - 1u))] = lane;
+    __syncthreads();
+    const bool low = adapter >= 0;
     if (low) {
         // row m of T: the slices' sums in order, times the adapter's scale; a warp per row
         const float sc = __ldg(p.scale + adapter);
-        for (int m = warp; m < 16 * NB; m += kLoraWarps) {
+        for (int m = warp; m < 16; m += kLoraWarps) {
             float big = 0.0f, v[8];   // r <= 256
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -211,208 +212,329 @@ __global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraPar
     }
     const T* Lb = static_cast<const T*>(p.Lb) + (low ? (size_t)adapter * p.N * p.r : 0);
     T* C = static_cast<T*>(p.C);
-    for (int pass = 0; pass < p.passes; ++pass) {
-        const int n0 = (blockIdx.x * p.passes + pass) * 256 + 32 * warp;
-        if (n0 >= p.N) break;   // (N is a multiple of 128: a warp's 32 channels are all there or none)
-        float acc[NB][4][4];
+    const int n0 = blockIdx.x * 256 + 32 * warp;
+    if (n0 >= p.N) return;   // (N is a multiple of 128: a warp's 32 channels are all there or none)
+    float acc[4][4];
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[b][j][0] = acc[b][j][1] = acc[b][j][2] = acc[b][j][3] = 0.0f;
-        if (low) {
-            const T* brow = Lb + (size_t)(n0 + 8 * (g >> 1) + (g & 1)) * p.r + 4 * t;
+    for (int j = 0; j < 4; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
+    if (low) {
+        const T* brow = Lb + (size_t)(n0 + 8 * (g >> 1) + (g & 1)) * p.r + 4 * t;
 #pragma unroll 4
-            for (int q = 0; q < r16; ++q) {
-                uint2 bv[4];
+        for (int q = 0; q < r16; ++q) {
+            uint2 bv[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    bv[j] = 16 * q + 4 * t < p.r ? __ldg(reinterpret_cast<const uint2*>(brow + (size_t)(2 * j) * p.r + 16 * q))
-                                                 : make_uint2(0, 0);
+            for (int j = 0; j < 4; ++j)
+                bv[j] = 16 * q + 4 * t < p.r ? __ldg(reinterpret_cast<const uint2*>(brow + (size_t)(2 * j) * p.r + 16 * q))
+                                             : make_uint2(0, 0);
+            const T* th = thi + g * ts + 16 * q + 4 * t;
+            const T* tl = tlo + g * ts + 16 * q + 4 * t;
+            const uint2 h0 = *reinterpret_cast<const uint2*>(th), h1 = *reinterpret_cast<const uint2*>(th + 8 * ts);
+            const uint2 l0 = *reinterpret_cast<const uint2*>(tl), l1 = *reinterpret_cast<const uint2*>(tl + 8 * ts);
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const T* th = thi + (16 * b + g) * ts + 16 * q + 4 * t;
-                    const T* tl = tlo + (16 * b + g) * ts + 16 * q + 4 * t;
-                    const uint2 h0 = *reinterpret_cast<const uint2*>(th), h1 = *reinterpret_cast<const uint2*>(th + 8 * ts);
-                    const uint2 l0 = *reinterpret_cast<const uint2*>(tl), l1 = *reinterpret_cast<const uint2*>(tl + 8 * ts);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        Ops::mma(acc[b][j], h0.x, h1.x, h0.y, h1.y, bv[j].x, bv[j].y);
-                        Ops::mma(acc[b][j], l0.x, l1.x, l0.y, l1.y, bv[j].x, bv[j].y);
-                    }
-                }
+            for (int j = 0; j < 4; ++j) {
+                Ops::mma(acc[j], h0.x, h1.x, h0.y, h1.y, bv[j].x, bv[j].y);
+                Ops::mma(acc[j], l0.x, l1.x, l0.y, l1.y, bv[j].x, bv[j].y);
             }
         }
+    }
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+    for (int h = 0; h < 2; ++h) {   // rows g and g + 8
+        const int m = 8 * h + g;
+        if (m >= n) continue;
+        const size_t at = (size_t)list[m] * p.N + n0 + 8 * t;
+        float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int s = 0; s < p.slices; ++s) {
+            const float4* q = reinterpret_cast<const float4*>(p.base + (size_t)s * p.M * p.N + at);
+            const float4 u = __ldcg(q), v = __ldcg(q + 1);
+            y[0] += u.x; y[1] += u.y; y[2] += u.z; y[3] += u.w;
+            y[4] += v.x; y[5] += v.y; y[6] += v.z; y[7] += v.w;
+        }
+        if (low) {
+            const float f = up[m];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {   // rows 16 b + g and 16 b + g + 8
-                const int m = 16 * b + 8 * h + g;
-                if (m >= n) continue;
-                const size_t at = (size_t)list[m] * p.N + n0 + 8 * t;
-                float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                for (int s = 0; s < p.slices; ++s) {
-                    const float4* q = reinterpret_cast<const float4*>(p.base + (size_t)s * p.M * p.N + at);
-                    const float4 u = __ldcg(q), v = __ldcg(q + 1);
-                    y[0] += u.x; y[1] += u.y; y[2] += u.z; y[3] += u.w;
-                    y[4] += v.x; y[5] += v.y; y[6] += v.z; y[7] += v.w;
-                }
-                if (low) {
-                    const float f = up[m];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        y[2 * j] = fmaf(acc[b][j][2 * h], f, y[2 * j]);
-                        y[2 * j + 1] = fmaf(acc[b][j][2 * h + 1], f, y[2 * j + 1]);
-                    }
-                }
-                uint4 o;
-                T* oh = reinterpret_cast<T*>(&o);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) oh[i] = Act<T>::from_f32(y[i]);
-                *reinterpret_cast<uint4*>(C + at) = o;
+            for (int j = 0; j < 4; ++j) {
+                y[2 * j] = fmaf(acc[j][2 * h], f, y[2 * j]);
+                y[2 * j + 1] = fmaf(acc[j][2 * h + 1], f, y[2 * j + 1]);
             }
+        }
+        uint4 o;
+        T* oh = reinterpret_cast<T*>(&o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) oh[i] = Act<T>::from_f32(y[i]);
+        *reinterpret_cast<uint4*>(C + at) = o;
+    }
+}
+
+// T as the tensor-core layer takes it. A row block (bn rows) has its adapters in order, each with
+// pr = ceil(r / 16) pieces of 16 ranks, `per` pieces (4 in a bf16 layer, 2 in an fp16 one) to a low-rank
+// unit of 128 columns: per piece [hi | lo] (bf16), or [hi | lo | hi | 0] (fp16, whose Lb is split into hi and
+// lo too). A warp writes one row, all units of its block; the block's first CTA lists units and pieces.
+template <typename T>
+__global__ void __launch_bounds__(kLoraThreads) lora_place_kernel(const LoraParams p, int bn, int max_units,
+                                                                  __nv_bfloat16* __restrict__ placed,
+                                                                  int* __restrict__ units, int* __restrict__ pieces,
+                                                                  int* __restrict__ bad) {
+    constexpr int kPer = std::is_same<T, __nv_bfloat16>::value ? 4 : 2;
+    __shared__ int slot[kRouteMaxBins];
+    __shared__ int wsum[kLoraWarps];
+    __shared__ __align__(16) __nv_bfloat16 hi[kLoraWarps][kLoraMaxRank], lo[kLoraWarps][kLoraMaxRank];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int row = blockIdx.x * kLoraWarps + warp, mb = blockIdx.x * kLoraWarps / bn, m0 = mb * bn;
+    const int pr = (p.r + 15) / 16;
+    for (int a = tid; a < p.L; a += kLoraThreads) slot[a] = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    for (int i = tid; i < bn && m0 + i < p.M; i += kLoraThreads) {
+        const int a = p.row_adapter[m0 + i];
+        if ((unsigned)a < (unsigned)p.L) slot[a] = 1;
+    }
+    __syncthreads();
+    // slot[a]: the adapter's place among the block's, four adapters per thread
+    int f[4], c = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        f[q] = 4 * tid + q < p.L ? slot[4 * tid + q] : 0;
+        c += f[q];
+    }
+    int x = c;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) wsum[warp] = x;
+    __syncthreads();
+    int before = x - c, total = 0;
+#pragma unroll
+    for (int w = 0; w < kLoraWarps; ++w) {
+        if (w < warp) before += wsum[w];
+        total += wsum[w];
+    }
+    const bool lists = blockIdx.x * kLoraWarps % bn == 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (4 * tid + q < p.L) {
+            slot[4 * tid + q] = before;
+            if (lists && f[q])
+                for (int j = 0; j < pr; ++j) pieces[(size_t)mb * max_units * kPer + before * pr + j] = 256 * (4 * tid + q) + j;
+            before += f[q];
+        }
+    const int lu = (total * pr + kPer - 1) / kPer;
+    if (lists) {
+        for (int j = total * pr + tid; j < lu * kPer; j += kLoraThreads) pieces[(size_t)mb * max_units * kPer + j] = -1;
+        if (tid == 0) units[mb] = lu;
+        if (blockIdx.x == 0 && tid == 0) *bad = 0;
+    }
+    __syncthreads();
+    if (row >= p.M) return;
+    int a = p.row_adapter[row];
+    if ((unsigned)a >= (unsigned)p.L) a = -1;
+    const int mine = a >= 0 ? slot[a] : -1;
+    if (a >= 0) {
+        const float sc = __ldg(p.scale + a);
+        for (int j = lane; j < 16 * pr; j += 32) {
+            float s = 0.0f;
+            if (j < p.r)
+                for (int k = 0; k < p.S; ++k) s += __ldcg(p.part + ((size_t)k * p.M + row) * p.r + j);
+            s *= sc;
+            const __nv_bfloat16 h = __float2bfloat16_rn(s);
+            hi[warp][j] = h;
+            lo[warp][j] = __float2bfloat16_rn(s - __bfloat162float(h));
+        }
+    }
+    __syncwarp();
+    uint4* out = reinterpret_cast<uint4*>(placed + (size_t)row * max_units * 128);
+    for (int q = lane; q < lu * 16; q += 32) {   // 8 columns: unit q / 16, block (q / 4) % 4, part q % 4
+        const int b = (q >> 2) & 3, part = q & 3;
+        const int piece = (q >> 4) * kPer + (kPer == 4 ? b : b >> 1);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (mine >= 0 && piece / pr == mine && !(kPer == 2 && (b & 1) && part >= 2)) {
+            const __nv_bfloat16* src = part < 2 ? hi[warp] : lo[warp];
+            v = *reinterpret_cast<const uint4*>(src + 16 * (piece - mine * pr) + 8 * (part & 1));
+        }
+        out[q] = v;
     }
 }
 
 // ------------------------------------------------------------------------------ host side
-struct LoraPlan {
-    int rows;       // rows of A taken at a time
-    int S;          // slices of K of the shrink kernel
-    int tiles;      // work items of a chunk (an upper bound above 16 rows)
-    int slices;     // FP32 outputs of the base kernel to add up
-    size_t base_ws; // workspace of the base kernel
-    size_t off_y, off_part, off_tiles, off_ntiles, off_rows, off_hist, total;
-};
-
-int lora_chunk_rows(int M, int N) {
-    size_t rows = kLoraChunkBytes / ((size_t)N * 4) / 256 * 256;
-    if (rows < 256) rows = 256;
-    return (size_t)M < rows ? M : (int)rows;
+// K slices of the shrink kernel: about two CTAs per SM when rows share adapters, a 32-K step per warp.
+int shrink_slices(int M, int K, int rows, int n_sm) {
+    int S = 2 * n_sm / ((M + rows - 1) / rows);
+    if (S > 16) S = 16;
+    if (S > K / 256) S = K / 256;
+    return S < 1 ? 1 : S;
 }
 
-LoraPlan plan_lora(int M, int N, int K, int group, int rank, int adapters) {
-    LoraPlan pl = {};
-    pl.rows = lora_chunk_rows(M, N);
-    const int m = pl.rows;
-    pl.slices = 1;
-    int n_sm = gemv_stream_sm_count();
-    if (n_sm <= 0) n_sm = 148;
-    if (m <= kLoraSmallRows) {
-        const GemvStreamPlan q = plan_gemv_stream(m, N, K, group, 0, n_sm);
-        if (q.ok) pl.slices = q.slices;
-        pl.tiles = m;
-        pl.S = 16;
-    } else {
-        const int most = m / 32 + adapters + 1;
-        pl.tiles = m < most ? m : most;
-        pl.S = 2 * n_sm / ((m + 31) / 32);   // two CTAs per SM when rows share adapters
-        if (pl.S > 16) pl.S = 16;
-    }
-    if (pl.S > K / 256) pl.S = K / 256;   // a 32-K step per warp
-    if (pl.S < 1) pl.S = 1;
-    auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-    pl.base_ws = up(w4a16_workspace_bytes(m, N, K, group));
-    pl.off_y = pl.base_ws;
-    pl.off_part = pl.off_y + up((size_t)pl.slices * m * N * 4);
-    pl.off_tiles = pl.off_part + up((size_t)pl.S * m * rank * 4);
-    pl.off_ntiles = pl.off_tiles + up((size_t)pl.tiles * sizeof(RouteTile));
-    pl.off_rows = pl.off_ntiles + 256;
-    pl.off_hist = pl.off_rows + up((size_t)m * 4);
-    pl.total = pl.off_hist + up(route_sort_workspace_bytes(m, 1, adapters, 1));
+// CTAs that share a row block's adapters: what is left of two per SM. (Eight at all sizes left 2048 rows of
+// four adapters with 1800 CTAs that had nothing to do: 60 us of the launch.)
+int shrink_shares(int M, int S, int rows, int n_sm) {
+    const int n = 2 * n_sm / (S * ((M + rows - 1) / rows));
+    return n < 1 ? 1 : n > rows ? rows : n;
+}
+
+int lora_sm_count() {
+    const int n = gemv_stream_sm_count();
+    return n > 0 ? n : 148;
+}
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+struct LoraGemvPlan {
+    int S, slices;
+    size_t off_y, off_part, total;
+};
+
+LoraGemvPlan plan_lora_gemv(int M, int N, int K, int group, int rank) {
+    LoraGemvPlan pl = {};
+    const GemvStreamPlan q = plan_gemv_stream(M, N, K, group, 0, lora_sm_count());
+    if (!q.ok) return pl;
+    pl.slices = q.slices;
+    pl.S = shrink_slices(M, K, 16, lora_sm_count());
+    pl.off_y = up256(kGemvStreamCounterBytes + q.partial_bytes);
+    pl.off_part = pl.off_y + up256((size_t)pl.slices * M * N * 4);
+    pl.total = pl.off_part + up256((size_t)pl.S * M * rank * 4);
     return pl;
 }
 
+struct LoraTcPlan {
+    int rows;        // rows of A taken at a time
+    int bn, mblocks; // of a piece of `rows` rows
+    int S, per, max_units;
+    size_t off_part, off_placed, off_units, off_pieces, off_bad, total;
+};
+
+LoraTcPlan plan_lora_tc(int M, int K, int rank, int adapters, int per) {
+    LoraTcPlan pl = {};
+    pl.per = per;
+    pl.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+    const int most = adapters < pl.bn ? adapters : pl.bn;   // adapters of a row block
+    pl.max_units = (most * ((rank + 15) / 16) + per - 1) / per;
+    size_t rows = kLoraPlaceBytes / ((size_t)pl.max_units * 256) / 256 * 256;
+    if (rows < 256) rows = 256;
+    if (rows > (size_t)kLoraMaxChunk) rows = kLoraMaxChunk;
+    pl.rows = (size_t)M < rows ? M : (int)rows;
+    pl.mblocks = (pl.rows + pl.bn - 1) / pl.bn;
+    pl.S = shrink_slices(pl.rows, K, 32, lora_sm_count());
+    pl.off_part = up256(kGemvStreamCounterBytes + (size_t)lora_sm_count() * pl.bn * 128 * sizeof(float));
+    // S M of any piece: one slice of up to `rows` rows, or at most two CTAs per SM of 32 rows each
+    size_t sm = (size_t)64 * lora_sm_count();
+    if (sm > (size_t)16 * pl.rows) sm = (size_t)16 * pl.rows;
+    if (sm < (size_t)pl.rows) sm = (size_t)pl.rows;
+    pl.off_placed = pl.off_part + up256(sm * rank * 4);
+    pl.off_units = pl.off_placed + up256((size_t)pl.rows * pl.max_units * 256);
+    pl.off_pieces = pl.off_units + up256((size_t)pl.mblocks * 4);
+    pl.off_bad = pl.off_pieces + up256((size_t)pl.mblocks * pl.max_units * per * 4);
+    pl.total = pl.off_bad + 256;
+    return pl;
+}
+
+template <int NB, typename T>
+cudaError_t launch_shrink(const LoraParams& p, int shares, cudaStream_t stream) {
+    const dim3 grid(p.S, (p.M + 8 * NB - 1) / (8 * NB), shares), block(kLoraThreads);
+    if (p.r <= 16) return launch_pdl(lora_shrink_kernel<NB, 1, T>, grid, block, 0, stream, p);
+    if (p.r <= 32) return launch_pdl(lora_shrink_kernel<NB, 2, T>, grid, block, 0, stream, p);
+    return launch_pdl(lora_shrink_kernel<NB, 4, T>, grid, block, 0, stream, p);
+}
+
 template <typename T>
-int launch_lora_chunk(LoraParams p, const LoraPlan& pl, uint8_t* ws, const void* tiled, int group, int sym, int dtype,
-                      int* dev_status, cudaStream_t stream) {
-    const bool small = p.M <= kLoraSmallRows;
+int launch_lora_gemv(LoraParams p, const LoraGemvPlan& pl, uint8_t* ws, const void* tiled, int group, int sym, int dtype,
+                     int* dev_status, cudaStream_t stream) {
     float* y = reinterpret_cast<float*>(ws + pl.off_y);
     p.S = pl.S;
     p.part = reinterpret_cast<float*>(ws + pl.off_part);
     p.base = y;
-    int items = p.M;
-    if (!small) {
-        RouteSort q = {};
-        q.ids = p.row_adapter;
-        q.T = p.M;
-        q.k = 1;
-        q.E = p.L;
-        q.H = 8;
-        q.spare = 1;
-        q.rows = reinterpret_cast<int32_t*>(ws + pl.off_rows);
-        q.hist = reinterpret_cast<int32_t*>(ws + pl.off_hist);
-        q.tiles = reinterpret_cast<RouteTile*>(ws + pl.off_tiles);
-        q.ntiles = reinterpret_cast<int*>(ws + pl.off_ntiles);
-        q.tile_rows = 32;
-        const int st = launch_route_sort(q, stream);
-        if (st != W4A16_OK) return st;
-        p.tiles = q.tiles;
-        p.ntiles = q.ntiles;
-        p.rows = q.rows;
-        const int most = p.M / 32 + p.L + 1;
-        items = p.M < most ? p.M : most;
-    }
-    const dim3 block(kLoraThreads), sgrid(p.S, items);
-    cudaError_t e = small ? launch_pdl(lora_shrink_kernel<2, T>, sgrid, block, 0, stream, p)
-                          : launch_pdl(lora_shrink_kernel<4, T>, sgrid, block, 0, stream, p);
+    const dim3 block(kLoraThreads);
+    const cudaError_t e = p.M <= 8 ? launch_shrink<1, T>(p, p.M, stream) : launch_shrink<2, T>(p, p.M, stream);
     if (e != cudaSuccess) return W4A16_ECUDA;
-    int slices = 1;
-    const int st = launch_gemm_f32(p.A, dtype, p.M, p.K, tiled, p.N, group, sym, y, &slices, ws, dev_status, stream);
+    const int st = launch_gemv_stream_f32(p.A, dtype, p.M, p.K, tiled, p.N, group, sym, y, &p.slices, ws, dev_status, stream);
     if (st != W4A16_OK) return st;
-    p.slices = slices;
-    const int blocks = (p.N + 255) / 256;
-    int n_sm = gemv_stream_sm_count();
-    if (n_sm <= 0) n_sm = 148;
-    // at least four CTAs per SM, then as many channel blocks per CTA as divide the rest (T's tile is
-    // made once per CTA)
-    const int busy = small ? 1 : (p.M + 31) / 32;
-    p.passes = blocks * busy / (4 * n_sm);
-    if (p.passes < 1) p.passes = 1;
-    if (p.passes > 8) p.passes = 8;
-    const dim3 egrid((blocks + p.passes - 1) / p.passes, items);
-    const int nb = small ? 1 : 2;
-    const size_t smem = (size_t)2 * 16 * nb * lora_t_stride(p.r) * 2;
-    e = small ? launch_pdl(lora_expand_kernel<1, T>, egrid, block, smem, stream, p)
-              : launch_pdl(lora_expand_kernel<2, T>, egrid, block, smem, stream, p);
-    return e == cudaSuccess ? W4A16_OK : W4A16_ECUDA;
+    const size_t smem = (size_t)2 * 16 * lora_t_stride(p.r) * 2;
+    return launch_pdl(lora_expand_kernel<T>, dim3((p.N + 255) / 256, p.M), block, smem, stream, p) == cudaSuccess
+               ? W4A16_OK
+               : W4A16_ECUDA;
+}
+
+// One piece of rows on the tensor cores. `pl` is the whole batch's plan: its offsets, bn and widths
+// hold for every piece.
+template <typename T>
+int launch_lora_tc(LoraParams p, const LoraTcPlan& pl, uint8_t* ws, const void* tiled, int group, int sym, int dtype,
+                   int* dev_status, cudaStream_t stream) {
+    const int mblocks = (p.M + pl.bn - 1) / pl.bn, n_sm = lora_sm_count();
+    const long long least = (long long)(p.N / 128) * mblocks * (p.K / 128);   // units without the low-rank ones
+    const TcPlan tp = plan_tc_rows(pl.bn, p.N, p.K, group, sym, (int)(least < n_sm ? least : n_sm), 32 + (size_t)(mblocks + 1) * 4);
+    if (!tp.ok) return W4A16_EUNSUPPORTED;
+    p.S = shrink_slices(p.M, p.K, 32, n_sm);
+    p.part = reinterpret_cast<float*>(ws + pl.off_part);
+    __nv_bfloat16* placed = reinterpret_cast<__nv_bfloat16*>(ws + pl.off_placed);
+    int* units = reinterpret_cast<int*>(ws + pl.off_units);
+    int* pieces = reinterpret_cast<int*>(ws + pl.off_pieces);
+    int* bad = reinterpret_cast<int*>(ws + pl.off_bad);
+    const dim3 block(kLoraThreads);
+    if (launch_shrink<4, T>(p, shrink_shares(p.M, p.S, 32, n_sm), stream) != cudaSuccess) return W4A16_ECUDA;
+    if (launch_pdl(lora_place_kernel<T>, dim3((p.M + kLoraWarps - 1) / kLoraWarps), block, 0, stream, p, pl.bn, pl.max_units,
+                   placed, units, pieces, bad) != cudaSuccess)
+        return W4A16_ECUDA;
+    CUtensorMap map, map_t;
+    if (!make_act_map(&map, p.A, p.M, p.K, pl.bn, dtype == W4A16_BF16) ||
+        !make_act_map(&map_t, placed, p.M, pl.max_units * 128, pl.bn, true))
+        return W4A16_ECUDA;
+    TcParams prm = tc_params(tp, tiled, p.M, p.N, p.K, group, sym, dtype == W4A16_BF16, ws, dev_status);
+    prm.mblocks = mblocks;
+    prm.C = p.C;
+    prm.off_grp = tp.off_bar + 1024;
+    prm.lora_units = units;
+    prm.lora_pieces = pieces;
+    prm.lora_b = p.Lb;
+    prm.row_adapter = p.row_adapter;
+    prm.lora_bad = bad;
+    prm.max_pieces = pl.max_units * pl.per;
+    prm.rank = p.r;
+    prm.adapters = p.L;
+    return launch_tc_bn<T, kTcLora>(pl.bn, map, map_t, prm, tp.smem, stream);
 }
 
 }  // namespace
 
 size_t lora_workspace_bytes(int M, int N, int K, int group, int rank, int adapters) {
-    // the last chunk may be short enough for the small-row kernels, whose plan differs
-    const LoraPlan a = plan_lora(M, N, K, group, rank, adapters);
-    size_t need = a.total;
-    const int rest = M % a.rows;
-    if (rest) {
-        const LoraPlan b = plan_lora(rest, N, K, group, rank, adapters);
-        if (b.total > need) need = b.total;
-    }
-    return need;
+    // the larger need over both types and both forms, so that a forced kernel also fits
+    const size_t a = plan_lora_tc(M, K, rank, adapters, 2).total, b = plan_lora_tc(M, K, rank, adapters, 4).total;
+    const size_t tc = a > b ? a : b;
+    const size_t gemv = M <= 16 ? plan_lora_gemv(M, N, K, group, rank).total : 0;
+    return tc > gemv ? tc : gemv;
 }
 
 int launch_lora_gemm(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
                      const void* La, const void* Lb, const float* scale, int adapters, int rank,
                      const int32_t* row_adapter, void* C, void* workspace, int* dev_status, cudaStream_t stream) {
-    const int chunk = lora_chunk_rows(M, N);
-    for (int m0 = 0; m0 < M; m0 += chunk) {
-        const int m = M - m0 < chunk ? M - m0 : chunk;
-        const LoraPlan pl = plan_lora(m, N, K, group, rank, adapters);
-        LoraParams p = {};
+    const bool bf16 = a_dtype == W4A16_BF16;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    LoraParams p = {};
+    p.A = A;
+    p.La = La;
+    p.Lb = Lb;
+    p.scale = scale;
+    p.row_adapter = row_adapter;
+    p.C = C;
+    p.M = M;
+    p.K = K;
+    p.N = N;
+    p.r = rank;
+    p.L = adapters;
+    if (M <= 16 && w4a16_select_kernel(M, N, K, group) == W4A16_KERNEL_GEMV) {
+        const LoraGemvPlan pl = plan_lora_gemv(M, N, K, group, rank);
+        if (pl.total)
+            return bf16 ? launch_lora_gemv<__nv_bfloat16>(p, pl, ws, tiled, group, sym, a_dtype, dev_status, stream)
+                        : launch_lora_gemv<__half>(p, pl, ws, tiled, group, sym, a_dtype, dev_status, stream);
+    }
+    const LoraTcPlan pl = plan_lora_tc(M, K, rank, adapters, bf16 ? 4 : 2);
+    for (int m0 = 0; m0 < M; m0 += pl.rows) {
+        p.M = M - m0 < pl.rows ? M - m0 : pl.rows;
         p.A = static_cast<const uint8_t*>(A) + (size_t)m0 * K * 2;
-        p.La = La;
-        p.Lb = Lb;
-        p.scale = scale;
-        p.row_adapter = row_adapter + m0;
         p.C = static_cast<uint8_t*>(C) + (size_t)m0 * N * 2;
-        p.M = m;
-        p.K = K;
-        p.N = N;
-        p.r = rank;
-        p.L = adapters;
-        uint8_t* ws = static_cast<uint8_t*>(workspace);
-        const int st = a_dtype == W4A16_BF16
-                           ? launch_lora_chunk<__nv_bfloat16>(p, pl, ws, tiled, group, sym, a_dtype, dev_status, stream)
-                           : launch_lora_chunk<__half>(p, pl, ws, tiled, group, sym, a_dtype, dev_status, stream);
+        p.row_adapter = row_adapter + m0;
+        const int st = bf16 ? launch_lora_tc<__nv_bfloat16>(p, pl, ws, tiled, group, sym, a_dtype, dev_status, stream)
+                            : launch_lora_tc<__half>(p, pl, ws, tiled, group, sym, a_dtype, dev_status, stream);
         if (st != W4A16_OK) return st;
     }
     return W4A16_OK;

@@ -65,8 +65,8 @@ int launch_moe_gemm(const void* A, int a_dtype, int R, int K, const void* tiled,
     prm.offsets = offsets;
     prm.E = E;
     prm.off_grp = pl.off_bar + 1024;
-    if (bf16) return launch_tc_bn<__nv_bfloat16, kTcGrouped>(pl.bn, map, prm, pl.smem, stream);
-    return launch_tc_bn<__half, kTcGrouped>(pl.bn, map, prm, pl.smem, stream);
+    if (bf16) return launch_tc_bn<__nv_bfloat16, kTcGrouped>(pl.bn, map, map, prm, pl.smem, stream);
+    return launch_tc_bn<__half, kTcGrouped>(pl.bn, map, map, prm, pl.smem, stream);
 }
 
 }  // namespace w4a16

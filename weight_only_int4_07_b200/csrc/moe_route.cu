@@ -23,16 +23,13 @@ __device__ __forceinline__ void count_bin(int* bins, int e, bool live) {
     if ((threadIdx.x & 31) == __ffs(peers) - 1) atomicAdd(&bins[e], __popc(peers));
 }
 
-__device__ __forceinline__ int bin_of(int id, int E, int spare) {
-    return (unsigned)id < (unsigned)E ? id : (spare ? E : -1);
-}
+__device__ __forceinline__ int bin_of(int id, int E) { return (unsigned)id < (unsigned)E ? id : -1; }
 
 // hist[b][e]: ids of block b (kRouteHistIds consecutive ids) in bin e.
 __global__ void __launch_bounds__(kSortThreads) route_hist_kernel(const int32_t* __restrict__ ids, int n, int E,
-                                                                  int spare, int32_t* __restrict__ hist) {
-    __shared__ int bins[kRouteMaxBins + 1];
-    const int B = E + (spare ? 1 : 0);
-    for (int e = threadIdx.x; e < B; e += kSortThreads) bins[e] = 0;
+                                                                  int32_t* __restrict__ hist) {
+    __shared__ int bins[kRouteMaxBins];
+    for (int e = threadIdx.x; e < E; e += kSortThreads) bins[e] = 0;
     __syncthreads();
     pdl_wait();
     pdl_trigger();
@@ -40,11 +37,11 @@ __global__ void __launch_bounds__(kSortThreads) route_hist_kernel(const int32_t*
 #pragma unroll
     for (int q = 0; q < kRouteHistIds / kSortThreads; ++q) {
         const int i = lo + q * kSortThreads + threadIdx.x;
-        const int e = i < n ? bin_of(ids[i], E, spare) : -1;
+        const int e = i < n ? bin_of(ids[i], E) : -1;
         count_bin(bins, e, e >= 0);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < B; e += kSortThreads) hist[(size_t)blockIdx.x * B + e] = bins[e];
+    for (int e = threadIdx.x; e < E; e += kSortThreads) hist[(size_t)blockIdx.x * E + e] = bins[e];
 }
 
 // The sort and the gather in one launch. Every CTA (blockIdx.x) owns tokens_per_cta consecutive
@@ -53,16 +50,16 @@ __global__ void __launch_bounds__(kSortThreads) route_hist_kernel(const int32_t*
 // row length when there are fewer tokens than SMs. Measured on the decode batch (64 ids): one
 // launch instead of count, scan, scatter and gather.
 __global__ void __launch_bounds__(kSortThreads) route_sort_kernel(const RouteSort p, int tokens_per_cta, int chunks) {
-    __shared__ int lower[kRouteMaxBins + 1];   // ids of the bin before the CTA's own, then the next slot
-    __shared__ int upper[kRouteMaxBins + 1];   // ids of the bin from the CTA's own on
+    __shared__ int lower[kRouteMaxBins];   // ids of the bin before the CTA's own, then the next slot
+    __shared__ int upper[kRouteMaxBins];   // ids of the bin from the CTA's own on
     __shared__ int list[kSortList];
-    __shared__ int wsum[2][kSortThreads / 32];
+    __shared__ int wsum[kSortThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n = p.T * p.k, E = p.E, B = E + (p.spare ? 1 : 0);
+    const int n = p.T * p.k, E = p.E;
     const int t0 = blockIdx.x * tokens_per_cta;
     const int t1 = min(t0 + tokens_per_cta, p.T);
     const int lo = t0 * p.k;
-    for (int e = tid; e < B; e += kSortThreads) lower[e] = upper[e] = 0;
+    for (int e = tid; e < E; e += kSortThreads) lower[e] = upper[e] = 0;
     __syncthreads();
     pdl_wait();
     pdl_trigger();
@@ -70,11 +67,11 @@ __global__ void __launch_bounds__(kSortThreads) route_sort_kernel(const RouteSor
     // counts of every bin, before the CTA's first id and from it on
     if (p.hist) {
         const int blocks = (n + kRouteHistIds - 1) / kRouteHistIds, own = lo / kRouteHistIds;
-        for (int e = tid; e < B; e += kSortThreads) {
+        for (int e = tid; e < E; e += kSortThreads) {
             int a = 0, b = 0;
 #pragma unroll 8
             for (int q = 0; q < blocks; ++q) {
-                const int c = __ldcg(p.hist + (size_t)q * B + e);
+                const int c = __ldcg(p.hist + (size_t)q * E + e);
                 if (q < own) a += c;
                 else b += c;
             }
@@ -84,7 +81,7 @@ __global__ void __launch_bounds__(kSortThreads) route_sort_kernel(const RouteSor
         __syncthreads();
         for (int i0 = own * kRouteHistIds; i0 < lo; i0 += kSortThreads) {
             const int i = i0 + tid;
-            const int e = i < lo ? bin_of(p.ids[i], E, p.spare) : -1;
+            const int e = i < lo ? bin_of(p.ids[i], E) : -1;
             const unsigned active = __ballot_sync(0xffffffffu, e >= 0);
             if (e >= 0) {
                 const unsigned peers = __match_any_sync(active, e);
@@ -100,7 +97,7 @@ __global__ void __launch_bounds__(kSortThreads) route_sort_kernel(const RouteSor
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int i = i0 + q * kSortThreads + tid;
-                e[q] = i < n ? bin_of(p.ids[i], E, p.spare) : -1;
+                e[q] = i < n ? bin_of(p.ids[i], E) : -1;
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -113,46 +110,28 @@ __global__ void __launch_bounds__(kSortThreads) route_sort_kernel(const RouteSor
     __syncthreads();
 
     // exclusive scan over the bins: `per` consecutive bins per thread. lower[e] becomes the slot of
-    // the CTA's next id of bin e. The first CTA writes the offsets and the tiles.
+    // the CTA's next id of bin e. The first CTA writes the offsets.
     const bool first = blockIdx.x == 0 && blockIdx.y == 0;
     {
-        const int per = (B + kSortThreads - 1) / kSortThreads;
-        const int e0 = tid * per, e1 = min(e0 + per, B);
-        int s = 0, ts = 0;
-        for (int e = e0; e < e1; ++e) {
-            const int c = lower[e] + upper[e];
-            s += c;
-            if (p.tiles) ts += (c + p.tile_rows - 1) / p.tile_rows;
-        }
-        int x = s, tx = ts;
+        const int per = (E + kSortThreads - 1) / kSortThreads;
+        const int e0 = tid * per, e1 = min(e0 + per, E);
+        int s = 0;
+        for (int e = e0; e < e1; ++e) s += lower[e] + upper[e];
+        int x = s;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, d), ty = __shfl_up_sync(0xffffffffu, tx, d);
-            if (lane >= d) {
-                x += y;
-                tx += ty;
-            }
+            const int y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
         }
-        if (lane == 31) {
-            wsum[0][warp] = x;
-            wsum[1][warp] = tx;
-        }
+        if (lane == 31) wsum[warp] = x;
         __syncthreads();
-        int base = x - s, tbase = tx - ts;
-        for (int w = 0; w < warp; ++w) {
-            base += wsum[0][w];
-            tbase += wsum[1][w];
-        }
+        int base = x - s;
+        for (int w = 0; w < warp; ++w) base += wsum[w];
         for (int e = e0; e < e1; ++e) {
             const int c = lower[e] + upper[e];
             if (first) {
-                if (p.offsets) p.offsets[e] = base;
-                if (p.tiles) {
-                    for (int q = 0; q < c; q += p.tile_rows)
-                        p.tiles[tbase++] = RouteTile{e, base + q, min(p.tile_rows, c - q), 0};
-                    if (e == B - 1) *p.ntiles = tbase;
-                }
-                if (p.offsets && e == B - 1) p.offsets[B] = base + c;
+                p.offsets[e] = base;
+                if (e == E - 1) p.offsets[E] = base + c;
             }
             lower[e] += base;
             base += c;
@@ -170,7 +149,7 @@ __global__ void __launch_bounds__(kSortThreads) route_sort_kernel(const RouteSor
         if (warp == 0) {
             for (int q = 0; q < own; q += 32) {
                 const int i = ta * p.k + q + lane;
-                const int e = q + lane < own ? bin_of(p.ids[i], E, p.spare) : -1;
+                const int e = q + lane < own ? bin_of(p.ids[i], E) : -1;
                 const unsigned active = __ballot_sync(0xffffffffu, e >= 0);
                 int slot = -1;
                 if (e >= 0) {
@@ -183,8 +162,8 @@ __global__ void __launch_bounds__(kSortThreads) route_sort_kernel(const RouteSor
                 if (q + lane < own) {
                     list[q + lane] = slot;
                     if (blockIdx.y == 0) {
-                        if (p.slots) p.slots[i] = slot;
-                        if (p.rows && slot >= 0) p.rows[slot] = i;
+                        p.slots[i] = slot;
+                        if (slot >= 0) p.rows[slot] = i;
                     }
                 }
             }
@@ -345,10 +324,10 @@ __global__ void __launch_bounds__(kCombThreads) moe_combine_grad_kernel(const ui
 
 }  // namespace
 
-size_t route_sort_workspace_bytes(int T, int k, int E, int spare) {
+size_t route_sort_workspace_bytes(int T, int k, int E) {
     const long long n = (long long)T * k;
     if (n <= kRouteDirectIds) return 0;
-    return (size_t)((n + kRouteHistIds - 1) / kRouteHistIds) * (size_t)(E + (spare ? 1 : 0)) * sizeof(int32_t);
+    return (size_t)((n + kRouteHistIds - 1) / kRouteHistIds) * (size_t)E * sizeof(int32_t);
 }
 
 int launch_route_sort(const RouteSort& q, cudaStream_t stream) {
@@ -358,7 +337,7 @@ int launch_route_sort(const RouteSort& q, cudaStream_t stream) {
         p.hist = nullptr;
     } else {
         const unsigned blocks = (unsigned)((n + kRouteHistIds - 1) / kRouteHistIds);
-        if (launch_pdl(route_hist_kernel, dim3(blocks), dim3(kSortThreads), 0, stream, p.ids, n, p.E, p.spare, p.hist) !=
+        if (launch_pdl(route_hist_kernel, dim3(blocks), dim3(kSortThreads), 0, stream, p.ids, n, p.E, p.hist) !=
             cudaSuccess)
             return W4A16_ECUDA;
     }

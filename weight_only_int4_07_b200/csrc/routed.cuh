@@ -12,11 +12,6 @@ constexpr int kRouteMaxChoices = 32;     // choices per token
 constexpr int kRouteDirectIds = 8192;    // ids that every CTA counts by itself
 constexpr int kRouteHistIds = 2048;      // ids of one histogram block above that
 
-// A run of up to `rows` consecutive sorted rows that share one bin.
-struct RouteTile {
-    int bin, begin, count, pad;
-};
-
 // Counting sort of n = T k ids into E bins, stable in the flat index: offsets[E + 1], rows (sorted
 // row -> flat index), slots (flat index -> sorted row, -1 without one) and, with X, the gathered rows.
 struct RouteSort {
@@ -24,17 +19,13 @@ struct RouteSort {
     int T, k, E;
     const void* X;       // [T, H] 16-bit, or null
     int H;
-    int32_t* offsets;    // null: not written
+    int32_t* offsets;
     int32_t* rows;
-    int32_t* slots;      // null: not written
+    int32_t* slots;
     void* Xs;
     int32_t* hist;       // route_sort_workspace_bytes
-    int spare;           // ids outside [0, E) go to bin E instead of nowhere (E + 1 bins)
-    RouteTile* tiles;    // null, or the runs of up to tile_rows rows of every bin, in bin order
-    int* ntiles;
-    int tile_rows;
 };
-size_t route_sort_workspace_bytes(int T, int k, int E, int spare);
+size_t route_sort_workspace_bytes(int T, int k, int E);
 int launch_route_sort(const RouteSort& p, cudaStream_t stream);
 
 int launch_moe_combine(const void* Ys, int dtype, int T, int k, int H, const int32_t* slots, const float* weights,
@@ -54,15 +45,10 @@ int launch_moe_gemv(const void* A, int a_dtype, int R, int K, const void* tiled,
 int launch_moe_gemm(const void* A, int a_dtype, int R, int K, const void* tiled, int E, const int32_t* offsets, int N,
                     int group, int sym, void* C, void* workspace, int kernel, int* dev_status, cudaStream_t stream);
 
-// The dense layer with FP32 outputs y [slices][M][N] (to be added up), chosen as w4a16_gemm chooses:
-// the decode kernel (launch_gemv_stream_f32, gemv_stream.cu) or the tensor-core GEMM
-// (launch_gemm_tc_f32, gemm_tc_f32.cu). `workspace` under the contract of w4a16_gemm.
+// The dense decode kernel with FP32 outputs y [slices][M][N] (to be added up) for a kernel that adds to
+// the layer's output before it is rounded. `workspace` under the contract of w4a16_gemm.
 int launch_gemv_stream_f32(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
                            float* y, int* slices, void* workspace, int* dev_status, cudaStream_t stream);
-int launch_gemm_tc_f32(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
-                       float* y, void* workspace, int* dev_status, cudaStream_t stream);
-int launch_gemm_f32(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym, float* y,
-                    int* slices, void* workspace, int* dev_status, cudaStream_t stream);
 
 // The layer with low-rank adapters.
 constexpr int kLoraMaxRank = 256;
