@@ -76,6 +76,9 @@ namespace {
 
 using namespace sm100;
 
+// Rows of one activation box of a grouped launch: a tile loads as many boxes as its rows need.
+__host__ __device__ constexpr int tc_box_rows(int bn) { return bn < 64 ? bn : 64; }
+
 // What the tiles are and where the sums go.
 constexpr int kTcDense = 0;     // rows [0, M) of A, C in the type of A
 constexpr int kTcLora = 1;      // the same, each tile with the low-rank units of its row block (lora.cu)
@@ -143,6 +146,27 @@ __device__ __forceinline__ int tc_unit_owner(long long u, long long U, int P) {
 
 __device__ __forceinline__ void tc_named_bar(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Two values rounded to T, the first in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t tc_pack2(float a, float b) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
+// The thread's tensor-memory loads have arrived; `v` is named so that no use of it moves ahead.
+__device__ __forceinline__ void tc_ld_wait16(uint32_t (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
+                 :
+                 : "memory");
 }
 
 // Warp-uniform bounded wait.
@@ -381,10 +405,20 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 const CUtensorMap* map = low ? &tmT : &tmA;
                 const int kx = kLora ? (low ? lw.ku - UT : lw.ku) : ku;
                 if (!mbar_wait(&free_s[s], ph ^ 1u, abort_flag, p.dev_status, wait_ns)) break;
-                mbar_arrive_expect_tx(&full_a[s], kSlotA);
                 uint8_t* dst = ring_a + (size_t)s * kSlotA;
-                tma_2d_g2s(dst, map, kx * 128, row, &full_a[s]);
-                tma_2d_g2s(dst + kSlotA / 2, map, kx * 128 + 64, row, &full_a[s]);
+                if constexpr (kGrp) {
+                    constexpr int kBox = tc_box_rows(BN);
+                    const int left = gw.row_end() - row, boxes = left >= BN ? BN / kBox : (left + kBox - 1) / kBox;
+                    mbar_arrive_expect_tx(&full_a[s], (uint32_t)(boxes * kBox) * 256u);
+                    for (int b = 0; b < boxes; ++b) {
+                        tma_2d_g2s(dst + b * kBox * 128, map, kx * 128, row + b * kBox, &full_a[s]);
+                        tma_2d_g2s(dst + kSlotA / 2 + b * kBox * 128, map, kx * 128 + 64, row + b * kBox, &full_a[s]);
+                    }
+                } else {
+                    mbar_arrive_expect_tx(&full_a[s], kSlotA);
+                    tma_2d_g2s(dst, map, kx * 128, row, &full_a[s]);
+                    tma_2d_g2s(dst + kSlotA / 2, map, kx * 128 + 64, row, &full_a[s]);
+                }
                 ++issued[s];
                 if (++s == NS) {
                     s = 0;
@@ -409,6 +443,9 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             bool ok = true;
             TcLoraWalk lw;
             if constexpr (kLora) lw.init(cum_tab, UT, p.mblocks, u0);
+            MoeWalk gw;
+            if constexpr (kGrp)
+                if (u0 < u1) gw.init(run_tab, blk_tab, p.E, p.N / 128, u0 / UT);
             if constexpr (US) {
                 // each own unit into accumulator ab * kIss + j (two per issuer, alternating)
                 for (long long i = u0; i < u1; ++i) {
@@ -443,6 +480,13 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 const long long tau = kLora ? 0 : i / UT;
                 const long long tile_end = kLora ? i + (lw.len - lw.ku) : (tau + 1) * UT;
                 const long long seg_end = u1 < tile_end ? u1 : tile_end;
+                uint32_t idesc_t = idesc;
+                if constexpr (kGrp && BN > 64) {   // as many columns as the tile has rows, in boxes
+                    if (i > u0) gw.next();
+                    constexpr int kBox = tc_box_rows(BN);
+                    const int left = gw.row_end() - gw.row0(BN);
+                    idesc_t = idesc_f16(left >= BN ? BN : (left + kBox - 1) / kBox * kBox, std::is_same<T, __nv_bfloat16>::value);
+                }
                 if (!mbar_wait(&accempty[ab], ((uint32_t)use[ab] & 1u) ^ 1u, abort_flag, p.dev_status, wait_ns)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem + (uint32_t)((ab * kIss + j) * kCols);
@@ -459,7 +503,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         // from the two 64-K boxes of the step's tile; one commit frees both tiles
                         const uint32_t a_tm = tmem_w + (uint32_t)(s * kTcStepCols);
                         const uint32_t b_sm = smem_u32(ring_a + (size_t)s * kSlotA);
-                        const uint32_t ids = kLora && lw.low() ? idesc_low : idesc;
+                        const uint32_t ids = kLora && lw.low() ? idesc_low : idesc_t;
                         mma4_f16_ts(d_tmem, a_tm, smem_desc_sw128(b_sm), ids, first ? 0u : 1u);
                         mma4_f16_ts(d_tmem, a_tm + 32u, smem_desc_sw128(b_sm + kSlotA / 2), ids, 1u);
                         mma_commit(&free_s[s]);
@@ -498,7 +542,26 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         // the counter of a cut tile: one per tile (dense), or one per CTA, of the one cut tile that
         // opens in the CTA's range
         auto counter = [&](long long tau, int cf) { return p.counters + (MODE == kTcDense ? tau : (long long)cf); };
-        auto put = [&](size_t at, float y) { C[at] = Act<T>::from_f32(y); };
+        // 16 rows from m of the warp's 32 channels, rounded. A lane holds one channel of every row; two
+        // exchanges (with lanes 1 and 2 away) give it four channels of every fourth row, so the rows go
+        // out in 8-byte stores of 64 bytes per row: a store of 2 bytes per lane and row kept the
+        // single accumulator of a 256-row tile for 5k cycles, a fifth of the tile.
+        auto put16 = [&](int m, int mend, size_t n0, const float (&y)[16]) {
+            uint32_t v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {   // rows 2 j, 2 j + 1
+                const uint32_t u = tc_pack2<T>(y[2 * j], y[2 * j + 1]);
+                const uint32_t o = __shfl_xor_sync(0xffffffffu, u, 1);
+                v[j] = lane & 1 ? __byte_perm(o, u, 0x7632) : __byte_perm(u, o, 0x5410);   // row 2 j + (lane & 1)
+            }
+            T* c = C + (size_t)(m + (lane & 3)) * p.N + n0 + 32 * q + 4 * (lane >> 2);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {   // row 4 i + (lane & 3)
+                const uint32_t o = __shfl_xor_sync(0xffffffffu, lane & 2 ? v[2 * i] : v[2 * i + 1], 2);
+                const uint2 w = lane & 2 ? make_uint2(o, v[2 * i + 1]) : make_uint2(v[2 * i], o);
+                if (m + 4 * i + (lane & 3) < mend) *reinterpret_cast<uint2*>(c + (size_t)(4 * i) * p.N) = w;
+            }
+        };
         // kTcLora: the tile's rows of every Lb it takes, on their way to L2 while the weight units run (a
         // fetch by the dequantizing warps that finds them in HBM waits behind the weight stream: 3.6 us
         // per low-rank unit at 16 rows of 14 adapters)
@@ -600,11 +663,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 #pragma unroll
                                 for (int jj = 0; jj < 16; ++jj) y[jj] += pv[jj];
                             }
-#pragma unroll
-                            for (int jj = 0; jj < 16; ++jj) {
-                                const int m = m0 + c * 16 + jj;
-                                if (m < mend) put((size_t)m * p.N + n0 + n, y[jj]);
-                            }
+                            put16(m0 + c * 16, mend, n0, y);
                         }
                     }
                 } else {
@@ -644,22 +703,37 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             if constexpr (kLora) lw.step((int)(seg_end - i));
             i = seg_end;
             const uint32_t lane_base = tmem + (uint32_t)(ab * kIss * kCols) + ((uint32_t)(32 * q) << 16);
-            // the tile's FP32 sums, 16 columns from c: the issuers' accumulators added
-            auto acc16 = [&](int c, float (&y)[16]) {
+            // the accumulator is free for the next tile's MMAs
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&accempty[ab]);
+            };
+            // the tile's FP32 sums, 16 columns at a time, to f(c, y): the issuers' accumulators added. The
+            // accumulator is released with the last ones read. (Loading the next 16 columns ahead, and
+            // releasing a 256-row tile's accumulator in halves, measured 5% slower and the same.)
+            auto sums = [&](auto f) {
+                const int nc = kGrp && mend - m0 < BN ? (mend - m0 + 15) / 16 : BN / 16;
                 uint32_t v[16];
+#pragma unroll 1
+                for (int c = 0; c < nc; ++c) {
+                    float y[16];
 #pragma unroll
-                for (int jj = 0; jj < 16; ++jj) y[jj] = 0.0f;
-                if (has0) {
-                    tmem_ld16(lane_base + (uint32_t)(c * 16), v);
-                    tmem_ld_wait();
+                    for (int jj = 0; jj < 16; ++jj) y[jj] = 0.0f;
+                    if (has0) {
+                        tmem_ld16(lane_base + (uint32_t)(c * 16), v);
+                        tc_ld_wait16(v);
 #pragma unroll
-                    for (int jj = 0; jj < 16; ++jj) y[jj] = __uint_as_float(v[jj]);
-                }
-                if (has1) {
-                    tmem_ld16(lane_base + (uint32_t)(kCols + c * 16), v);
-                    tmem_ld_wait();
+                        for (int jj = 0; jj < 16; ++jj) y[jj] = __uint_as_float(v[jj]);
+                    }
+                    if (has1) {
+                        tmem_ld16(lane_base + (uint32_t)(kCols + c * 16), v);
+                        tc_ld_wait16(v);
 #pragma unroll
-                    for (int jj = 0; jj < 16; ++jj) y[jj] += __uint_as_float(v[jj]);
+                        for (int jj = 0; jj < 16; ++jj) y[jj] += __uint_as_float(v[jj]);
+                    }
+                    if (c + 1 == nc) release();
+                    f(c, y);
                 }
             };
             if (cf == cl || cta == cf) {
@@ -684,10 +758,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     tc_named_bar(1, 128);
                 }
                 if (ok && !*abort_flag) {
-#pragma unroll 1
-                    for (int c = 0; c < BN / 16; ++c) {
-                        float y[16];
-                        acc16(c, y);
+                    sums([&](int c, float (&y)[16]) {
                         // the other CTAs' sums, in CTA order; the 16 loads of one CTA in flight together
 #pragma unroll 1
                         for (int cc = cf + 1; cc <= cl; ++cc) {
@@ -698,36 +769,30 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 #pragma unroll
                             for (int j = 0; j < 16; ++j) y[j] += pv[j];
                         }
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const int m = m0 + c * 16 + j;
-                            if (m < mend) put((size_t)m * p.N + n0 + n, y[j]);
-                        }
-                    }
+                        put16(m0 + c * 16, mend, n0, y);
+                    });
+                } else {
+                    release();
                 }
             } else {
                 // a later CTA of a cut tile (the tile opens its range): publish the sums and count
                 // them, without waiting
                 if (ok && !*abort_flag) {
                     float* part = p.partials + (size_t)cta * BN * 128;
-#pragma unroll 1
-                    for (int c = 0; c < BN / 16; ++c) {
-                        float y[16];
-                        acc16(c, y);
+                    sums([&](int c, float (&y)[16]) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
                             const int mr = c * 16 + j;
                             if (m0 + mr < mend) __stcg(part + (size_t)mr * 128 + n, y[j]);
                         }
-                    }
+                    });
+                } else {
+                    release();
                 }
                 __threadfence();
                 tc_named_bar(1, 128);
                 if (leader) asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(counter(tau, cf)) : "memory");
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&accempty[ab]);
             ++use[ab];
             if (kBufs == 2) ab ^= 1;
         }

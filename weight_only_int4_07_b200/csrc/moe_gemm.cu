@@ -59,7 +59,7 @@ int launch_moe_gemm(const void* A, int a_dtype, int R, int K, const void* tiled,
     if (!pl.ok) return W4A16_EUNSUPPORTED;
     const bool bf16 = a_dtype == W4A16_BF16;
     CUtensorMap map;
-    if (!make_act_map(&map, A, R, K, pl.bn, bf16)) return W4A16_ECUDA;
+    if (!make_act_map(&map, A, R, K, tc_box_rows(pl.bn), bf16)) return W4A16_ECUDA;
     TcParams prm = tc_params(pl, tiled, R, N, K, group, sym, bf16, workspace, dev_status);
     prm.C = C;
     prm.offsets = offsets;
