@@ -77,6 +77,10 @@ CASES = [  # M, K, N, group, sym, dtype, rank, adapters, ids
     (1, 512, 256, 64, 1, torch.float16, 64, 2, "none"),
     (3, 1024, 384, 32, 0, torch.bfloat16, 24, 2, "any"),
     (8, 8192, 384, 128, 0, torch.float16, 32, 3, "any"),          # K slices in the decode kernel
+    (8, 8192, 384, 128, 0, torch.bfloat16, 64, 9, "any"),
+    (2, 2048, 1152, 32, 0, torch.float16, 64, 2, "any"),
+    (7, 4096, 128, 64, 1, torch.bfloat16, 8, 7, "wild"),
+    (5, 1024, 256, 128, 0, torch.float16, 16, 4, "any"),          # too many products for the decode kernel
     (16, 640, 256, 128, 1, torch.bfloat16, 40, 16, "wild"),
     (16, 4096, 128, 128, 0, torch.float16, 256, 2, "one"),        # the tensor-core layer, 16 rows
     (17, 256, 128, 128, 0, torch.bfloat16, 8, 4, "any"),

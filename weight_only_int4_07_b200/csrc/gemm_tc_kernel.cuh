@@ -135,10 +135,6 @@ struct TcParams {
     GsMasks km;
 };
 
-__device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
-
 __device__ __forceinline__ long long tc_unit_begin(int c, long long U, int P) { return ((long long)c * U) / P; }
 __device__ __forceinline__ int tc_unit_owner(long long u, long long U, int P) {
     return (int)(((u + 1) * P - 1) / U);

@@ -113,12 +113,23 @@ struct GsParams {
     int lda, c0, ktot, slices;
     float* out_f32;
     uint64_t wait_ns;   // limit of every bounded wait (the drain after a timeout keeps kGsSpin)
+    GemvLora lora;      // LO: the rows' rank products, and the bytes they take in shared memory
+    uint32_t lora_bytes;
 };
+
+// LO: elements between the rows of t (an odd number of 16-byte steps: the lanes' 8-byte reads of eight
+// rows miss no bank).
+__host__ __device__ inline int gs_lora_stride(int rank) { return (rank + 15) / 16 * 16 + 8; }
 
 // NB: n8 tiles of activation rows (1: M <= 8, 2: M <= 16). ODD: rows 2t + 1 of an n8 tile exist.
 // SL: the launch serves several K slices (a separate instance, so that the single-slice one keeps
-// no slice arithmetic).
-template <int NB, typename T, int GROUP, bool ODD, bool SL>
+// no slice arithmetic). LO: low-rank terms, C[m, n] += sum_j t[m, j] Lb[a][n, j], a = row m's adapter. t
+// (summed over its slices of K) lies in shared memory as bf16 hi + lo; at the end of each tile that
+// the CTA writes, the groups share out the pieces (16 ranks of one adapter of the batch) and add them to
+// their sums by a few bf16 MMAs, Lb read straight from global memory (fetched to L2 by the epilogue warp
+// when the tile began), an fp16 Lb as hi + lo, exactly; (The epilogue
+// warp forming the terms by itself took 0.9 us per tile and row at rank 16.)
+template <int NB, typename T, int GROUP, bool ODD, bool SL, bool LO>
 __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(const GsParams p) {
     extern __shared__ __align__(128) uint8_t smem_raw[];
     constexpr bool kPost = (GROUP == 128);   // one group per unit: scale the unit's sum
@@ -157,7 +168,9 @@ __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(c
     uint8_t* zrow = smem_raw + p.act_bytes + p.red_bytes + p.sa_bytes;    // 320 zero bytes
     int* rowexp = reinterpret_cast<int*>(zrow + 320);                     // [16] largest exponent per row
     int* rowmin = reinterpret_cast<int*>(zrow + 384);                     // [16] smallest nonzero one
-    uint8_t* stages = zrow + kGsZrowBytes;                                // ns x stage_bytes
+    const int lts = LO ? gs_lora_stride(p.lora.rank) : 0;                 // LO: t, hi then lo, [M][lts]
+    __nv_bfloat16* lt = reinterpret_cast<__nv_bfloat16*>(zrow + kGsZrowBytes);
+    uint8_t* stages = zrow + kGsZrowBytes + (LO ? p.lora_bytes : 0);      // ns x stage_bytes
     uint64_t* full = reinterpret_cast<uint64_t*>(stages + (size_t)ns * stage_bytes);   // [ns] stage landed
     uint64_t* empty = full + ns;        // [ns] the 16 compute warps left the slot's stage
     uint64_t* tfull = empty + ns;       // [2] the groups' sums of a tile are in `red`
@@ -228,8 +241,41 @@ __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(c
     const int nneed = nunits < steps ? nunits : steps;
     const int nchunk = 16 * nneed;   // 8-element chunks of A
 
+    // LO: lane m holds row m's adapter (-1: none; the first slice's CTAs add the terms). Lb's channels of the
+    // first tile to L2 before the wait: the kernel before this one (lora.cu) lets it start only after
+    // everything before that one has completed.
+    int mine = -1;
+    if constexpr (LO) {
+        if (lane < M && sl == 0) mine = __ldg(p.lora.row_adapter + lane);
+        if ((unsigned)mine >= (unsigned)p.lora.adapters) mine = -1;
+    }
+    auto ahead = [&](int tile) {
+        if (mine >= 0 && tile < N / 128)
+            bulk_prefetch_l2(static_cast<const T*>(p.lora.b) + ((size_t)mine * N + (size_t)tile * 128) * p.lora.rank,
+                             256u * (uint32_t)p.lora.rank);
+    };
+    if (LO && warp == kGsWarpEpilogue) ahead((int)(u0 / steps));
+
     // A may be the output of the previous kernel in the stream
     grid_dependency_wait();
+
+    // LO: this thread's values of t (M rank <= 2 threads), summed over their slices in order
+    float tv[2] = {0.0f, 0.0f};
+    if constexpr (LO) {
+        if (sl == 0)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = threadIdx.x + h * kGsThreads;
+                if (i < M * p.lora.rank) {
+                    const int a = p.lora.row_adapter[i / p.lora.rank];
+                    if ((unsigned)a < (unsigned)p.lora.adapters) {
+#pragma unroll 16
+                        for (int k = 0; k < p.lora.slices; ++k) tv[h] += __ldcg(p.lora.part + (size_t)k * M * p.lora.rank + i);
+                        tv[h] *= __ldg(p.lora.scale + a);
+                    }
+                }
+            }
+    }
 
     // Staging: activations: 32-K block t of unit sp at sp * 320 + 80 t (the 16-byte padding makes
     // the lanes' 16-byte reads conflict free); pairs in each 16-byte chunk stored (p0, p2, p1, p3)
@@ -332,6 +378,27 @@ __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(c
                 }
                 *q = v;
                 unit_sum(half8_sum(v), m, sp);
+            }
+        }
+    }
+    if constexpr (LO) {
+        // t in the scale of this CTA's sums (kConv: times its rows' 2^-k), as hi + lo; ranks past the
+        // last are zeros
+        for (int i = threadIdx.x; i < M * (lts - p.lora.rank); i += kGsThreads) {
+            const int m = i / (lts - p.lora.rank), j = p.lora.rank + i - m * (lts - p.lora.rank);
+            lt[m * lts + j] = lt[(M + m) * lts + j] = __float2bfloat16_rn(0.0f);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = threadIdx.x + h * kGsThreads;
+            if (i < M * p.lora.rank) {
+                const int m = i / p.lora.rank, j = i - m * p.lora.rank;
+                float x = tv[h];
+                if constexpr (kConv)
+                    if (!wide) x *= __int_as_float((127 - min(max(rowexp[m] - 141, -100), 114)) << 23);
+                const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+                lt[m * lts + j] = hi;
+                lt[(M + m) * lts + j] = __float2bfloat16_rn(x - __bfloat162float(hi));
             }
         }
     }
@@ -532,6 +599,63 @@ __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(c
         }
     };
 
+    // LO, compute warps: the pieces of this group added to tot, for channels ch0 + 8 r of the tile
+    auto low_rank = [&](int tile) {
+        using B = GsOps<__nv_bfloat16>;
+        const unsigned peers = __match_any_sync(0xffffffffu, mine);
+        unsigned left = __ballot_sync(0xffffffffu, mine >= 0 && __ffs(peers) - 1 == lane);
+        // the adapters of this lane's result columns, rows 2 t and 2 t + 1: a piece's sums count for the rows
+        // of its adapter only (zeros in place of the other rows' t would not keep out an Lb that is not
+        // finite)
+        const int of0 = __shfl_sync(0xffffffffu, mine, 2 * t), of1 = __shfl_sync(0xffffffffu, mine, 2 * t + 1);
+        const __nv_bfloat16* th = lt + (g < M ? g : 0) * lts + 4 * t;
+        int q = 0;
+        for (; left; left &= left - 1) {
+            const int a = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
+            const T* b = static_cast<const T*>(p.lora.b) + ((size_t)a * N + (size_t)tile * 128 + ch0) * p.lora.rank + 4 * t;
+            float d[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+            for (int j = 0; j < p.lora.rank; j += 16, ++q) {
+                if ((q & 3) != grp) continue;
+                uint2 w[4];   // channels ch0 + 8 r, ranks j + 4 t ..
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    w[r] = j + 4 * t < p.lora.rank
+                               ? __ldg(reinterpret_cast<const uint2*>(b + (size_t)(8 * r) * p.lora.rank + j))
+                               : make_uint2(0, 0);
+                const uint2 hi = *reinterpret_cast<const uint2*>(th + j), lo = *reinterpret_cast<const uint2*>(th + M * lts + j);
+                uint2 wl[4];
+                if constexpr (std::is_same<T, __half>::value) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        uint32_t* x = reinterpret_cast<uint32_t*>(&w[r]);
+                        uint32_t* y = reinterpret_cast<uint32_t*>(&wl[r]);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[e]));
+                            const uint32_t hx = __float_as_uint(f.x) & 0xFFFF0000u, hy = __float_as_uint(f.y) & 0xFFFF0000u;
+                            y[e] = (__float_as_uint(f.x - __uint_as_float(hx)) >> 16) |
+                                   (__float_as_uint(f.y - __uint_as_float(hy)) & 0xFFFF0000u);
+                            x[e] = (hx >> 16) | hy;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int rt = 0; rt < 2; ++rt) {
+                    const uint2 w0 = w[2 * rt], w1 = w[2 * rt + 1];
+                    B::mma(d[rt], w0.x, w1.x, w0.y, w1.y, hi.x, hi.y);
+                    B::mma(d[rt], w0.x, w1.x, w0.y, w1.y, lo.x, lo.y);
+                    if constexpr (std::is_same<T, __half>::value)
+                        B::mma(d[rt], wl[2 * rt].x, wl[2 * rt + 1].x, wl[2 * rt].y, wl[2 * rt + 1].y, hi.x, hi.y);
+                }
+            }
+#pragma unroll
+            for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if ((e & 1 ? of1 : of0) == a) tot[rt][0][e] += d[rt][e];
+        }
+    };
+
     if (warp == kGsWarpProducer) {
         // ------------------------------------------------------------ producer (lane 0)
         // refills slot s with stage st once the 16 compute warps have left stage st - ns
@@ -563,6 +687,7 @@ __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(c
             // the other shared buffer (free: no tile follows), so that reaching them from L2 is off
             // the path once the compute warps finish.
             const bool gather = cf != cl && cta == cf;
+            if (LO && ehi < nunits) ahead(etile + 1);
             float* pre = red + (size_t)(bsel ^ 1) * kGsGroups * M * 128;
             if (gather) {
                 if (lane == 0) {
@@ -697,6 +822,7 @@ __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(c
                 __syncwarp();
                 if (lane == 0 && !aborted) mbar_arrive(&empty[s_idx]);
             }
+            if (LO && sl == 0 && (long long)tile * steps >= u0) low_rank(tile);   // (a tile that this CTA writes)
             tile_end();
             if (seg_lo >= nunits) break;
         }
@@ -712,12 +838,12 @@ __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(c
     }
 }
 
-template <int NB, typename T, int GROUP, bool ODD, bool SL>
+template <int NB, typename T, int GROUP, bool ODD, bool SL, bool LO>
 int launch_typed(const GsParams& prm, size_t smem, cudaStream_t stream) {
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(gemv_stream_kernel<NB, T, GROUP, ODD, SL>,
+        attr_err = cudaFuncSetAttribute(gemv_stream_kernel<NB, T, GROUP, ODD, SL, LO>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kGsSmemMax);
     });
     if (attr_err != cudaSuccess) return W4A16_ECUDA;
@@ -731,31 +857,32 @@ int launch_typed(const GsParams& prm, size_t smem, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, gemv_stream_kernel<NB, T, GROUP, ODD, SL>, prm);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, gemv_stream_kernel<NB, T, GROUP, ODD, SL, LO>, prm);
     return e == cudaSuccess ? W4A16_OK : W4A16_ECUDA;
 }
 
-template <int NB, typename T, bool ODD, bool SL>
+template <int NB, typename T, bool ODD, bool SL, bool LO>
 int launch_group(const GsParams& prm, int group, size_t smem, cudaStream_t stream) {
     switch (group) {
-        case 32: return launch_typed<NB, T, 32, ODD, SL>(prm, smem, stream);
-        case 64: return launch_typed<NB, T, 64, ODD, SL>(prm, smem, stream);
-        case 128: return launch_typed<NB, T, 128, ODD, SL>(prm, smem, stream);
+        case 32: return launch_typed<NB, T, 32, ODD, SL, LO>(prm, smem, stream);
+        case 64: return launch_typed<NB, T, 64, ODD, SL, LO>(prm, smem, stream);
+        case 128: return launch_typed<NB, T, 128, ODD, SL, LO>(prm, smem, stream);
         default: return W4A16_EUNSUPPORTED;
     }
 }
 
-template <int NB, typename T, bool ODD>
+template <int NB, typename T, bool ODD, bool LO>
 int launch_sliced(const GsParams& prm, int group, size_t smem, cudaStream_t stream) {
-    return prm.slices > 1 ? launch_group<NB, T, ODD, true>(prm, group, smem, stream)
-                          : launch_group<NB, T, ODD, false>(prm, group, smem, stream);
+    return prm.slices > 1 ? launch_group<NB, T, ODD, true, LO>(prm, group, smem, stream)
+                          : launch_group<NB, T, ODD, false, LO>(prm, group, smem, stream);
 }
 
-template <typename T>
+template <typename T, bool LO>
 int launch_rows(const GsParams& prm, int group, size_t smem, cudaStream_t stream) {
-    if (prm.M > 8) return launch_sliced<2, T, true>(prm, group, smem, stream);
-    if (prm.M > 1) return launch_sliced<1, T, true>(prm, group, smem, stream);
-    return launch_sliced<1, T, false>(prm, group, smem, stream);
+    if constexpr (!LO)   // (low-rank terms: up to 8 rows)
+        if (prm.M > 8) return launch_sliced<2, T, true, LO>(prm, group, smem, stream);
+    if (prm.M > 1) return launch_sliced<1, T, true, LO>(prm, group, smem, stream);
+    return launch_sliced<1, T, false, LO>(prm, group, smem, stream);
 }
 
 // C = sum over the S slices of the FP32 partial outputs, in slice order.
@@ -786,7 +913,7 @@ int sm_count() {
 namespace {
 
 // The layout of one launch over a K slice of Ks input channels.
-GemvStreamPlan plan_slice(int M, int N, int Ks, int group, int sym, int n_sm) {
+GemvStreamPlan plan_slice(int M, int N, int Ks, int group, int sym, int n_sm, size_t extra) {
     GemvStreamPlan pl = {};
     const TiledLayout L = tiled_layout(Ks, N, group, sym);   // the record size does not depend on K
     const size_t units = (size_t)(Ks / 128);
@@ -796,7 +923,7 @@ GemvStreamPlan plan_slice(int M, int N, int Ks, int group, int sym, int n_sm) {
     pl.sa_bytes = (((size_t)units * ((M + 1) & ~1) * 4) + 127) & ~(size_t)127;   // unit sums (group 128)
     pl.stage_bytes = ((size_t)kGsUnitsPerStage * L.record + 127) & ~(size_t)127;
     const size_t flags = ((size_t)2 * kGsMaxStages * 8 + 32 + 8 + 4 * kGsMaxStages + 127) & ~(size_t)127;
-    const size_t fixed = pl.act_bytes + pl.red_bytes + pl.sa_bytes + kGsZrowBytes + flags;
+    const size_t fixed = pl.act_bytes + pl.red_bytes + pl.sa_bytes + kGsZrowBytes + flags + extra;
     if (fixed >= (size_t)kGsSmemMax) return pl;
     size_t ns = ((size_t)kGsSmemMax - fixed) / pl.stage_bytes;
     if (ns > kGsMaxStages) ns = kGsMaxStages;
@@ -816,13 +943,23 @@ GemvStreamPlan plan_slice(int M, int N, int Ks, int group, int sym, int n_sm) {
 // is cut into S equal slices (S a power of two dividing K / 128), each served by its own group of
 // n_sm / S CTAs of the same launch, whose FP32 outputs a last kernel adds in slice order.
 GemvStreamPlan plan_gemv_stream(int M, int N, int K, int group, int sym, int n_sm) {
+    return plan_gemv_lora(M, N, K, group, sym, n_sm, 0);
+}
+
+static size_t lora_smem(int M, int rank) {
+    return rank > 0 ? ((size_t)2 * M * gs_lora_stride(rank) * 2 + 127) & ~(size_t)127 : 0;
+}
+
+// The same with the rank products of M rows (rank 0: none) beside the activations.
+GemvStreamPlan plan_gemv_lora(int M, int N, int K, int group, int sym, int n_sm, int rank) {
+    const size_t extra = lora_smem(M, rank);
     GemvStreamPlan pl = {};
     if (M < 1 || M > 16 || K % 128 != 0 || N % 128 != 0 || K < 128 || N < 128) return pl;
     if (group != 32 && group != 64 && group != 128) return pl;
     if (N / 128 > kGemvStreamMaxTiles) return pl;
     for (int S = 1; S <= 64 && (K / 128) % S == 0; S *= 2) {
         if ((long long)(N / 128) * S > kGemvStreamMaxTiles) break;   // tile counters of every slice
-        pl = plan_slice(M, N, K / S, group, sym, S > 1 ? n_sm / S : n_sm);
+        pl = plan_slice(M, N, K / S, group, sym, S > 1 ? n_sm / S : n_sm, extra);
         if (pl.ok) {
             pl.slices = S;
             pl.partial_bytes = (size_t)2 * kGsCtasPerSm * (n_sm > 0 ? n_sm : 0) * M * 128 * 4 +
@@ -835,10 +972,12 @@ GemvStreamPlan plan_gemv_stream(int M, int N, int K, int group, int sym, int n_s
 
 int gemv_stream_sm_count() { return sm_count(); }
 
-// y32: FP32 outputs of the S slices ([S][M][N], S >= 1) instead of C; slices gets S.
+// lora: the rows' rank products, whose terms the launch adds (null: the layer alone).
 static int launch_gemv(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym, void* C,
-                       float* y32, int* slices, void* workspace, int* dev_status, cudaStream_t stream) {
-    const GemvStreamPlan pl = plan_gemv_stream(M, N, K, group, sym, sm_count());
+                       const GemvLora* lora, void* workspace, int* dev_status, cudaStream_t stream) {
+    const int rank = lora ? lora->rank : 0;
+    if (lora && (M > 8 || M * rank > 2 * kGsThreads)) return W4A16_EUNSUPPORTED;
+    const GemvStreamPlan pl = plan_gemv_lora(M, N, K, group, sym, sm_count(), rank);
     if (!pl.ok) return W4A16_EUNSUPPORTED;
     if (!workspace) return W4A16_EWORKSPACE;
     const int S = pl.slices;
@@ -882,12 +1021,15 @@ static int launch_gemv(const void* A, int a_dtype, int M, int K, const void* til
     prm.A = A;
     prm.c0 = 0;
     prm.slices = S;
-    prm.out_f32 = y32 ? y32 : S > 1 ? slice_out : nullptr;
-    if (slices) *slices = S;
-    const int st = bf16 ? launch_rows<__nv_bfloat16>(prm, group, pl.smem, stream)
-                        : launch_rows<__half>(prm, group, pl.smem, stream);
+    prm.out_f32 = S > 1 ? slice_out : nullptr;
+    if (lora) prm.lora = *lora;
+    prm.lora_bytes = (uint32_t)lora_smem(M, rank);
+    const int st = lora ? (bf16 ? launch_rows<__nv_bfloat16, true>(prm, group, pl.smem, stream)
+                                : launch_rows<__half, true>(prm, group, pl.smem, stream))
+                        : (bf16 ? launch_rows<__nv_bfloat16, false>(prm, group, pl.smem, stream)
+                                : launch_rows<__half, false>(prm, group, pl.smem, stream));
     if (st != W4A16_OK) return st;
-    if (S > 1 && !y32) {
+    if (S > 1) {
         const size_t MN = (size_t)M * N;
         const unsigned blocks = (unsigned)((MN + 255) / 256 < 2048 ? (MN + 255) / 256 : 2048);
         if (bf16)
@@ -902,12 +1044,12 @@ static int launch_gemv(const void* A, int a_dtype, int M, int K, const void* til
 
 int launch_gemv_stream(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
                        void* C, void* workspace, int* dev_status, cudaStream_t stream) {
-    return launch_gemv(A, a_dtype, M, K, tiled, N, group, sym, C, nullptr, nullptr, workspace, dev_status, stream);
+    return launch_gemv(A, a_dtype, M, K, tiled, N, group, sym, C, nullptr, workspace, dev_status, stream);
 }
 
-int launch_gemv_stream_f32(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
-                           float* y, int* slices, void* workspace, int* dev_status, cudaStream_t stream) {
-    return launch_gemv(A, a_dtype, M, K, tiled, N, group, sym, nullptr, y, slices, workspace, dev_status, stream);
+int launch_gemv_lora(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym, void* C,
+                     const GemvLora& lora, void* workspace, int* dev_status, cudaStream_t stream) {
+    return launch_gemv(A, a_dtype, M, K, tiled, N, group, sym, C, &lora, workspace, dev_status, stream);
 }
 
 }  // namespace w4a16

@@ -4,7 +4,7 @@
 //   shrink  T[m, j] = s_a sum_k A[m, k] La_a[j, k], FP32 partial sums over slices of K. Both operands of
 //           its warp MMAs (m16n8k16) come straight from global memory: a lane reads 16 consecutive
 //           bytes of a row and the same permutation of K stands on both sides. Rows of one adapter
-//           within a block of 16 or 32 rows are taken together.
+//           within a block of 8 or 32 rows are taken together.
 // Then, where the layer runs on the tensor cores (launch_lora_tc):
 //   place   per block of BN rows, T as a matrix with one run of columns per adapter of the block, its
 //           rows' values there (as bf16 hi + lo) and zeros in the other rows;
@@ -13,10 +13,8 @@
 //           kernel that added T . Lb^T to FP32 outputs of the layer took 93 us of every 512 rows
 //           of the 4096 x 28672 layer, beside the layer's 117.)
 // and for few rows, where the decode kernel streams the layer (launch_lora_gemv):
-//   layer   that kernel with FP32 outputs;
-//   expand  C = outputs + 2^e (T 2^-e) . Lb_a^T, rounded once, again on warp MMAs from global memory: T
-//           enters as hi + lo in 16 bits under a power of two per row that puts its largest value near
-//           2^14 (fp16 then keeps everything down to 2^-38 of it).
+//   layer   that kernel (gemv_stream.cu), whose compute warps add a tile's T . Lb^T to their sums by a few
+//           more MMAs.
 // The kernels follow each other by programmatic dependent launch.
 #include <type_traits>
 
@@ -38,9 +36,8 @@ struct LoraParams {
     const float* scale;         // [L]
     const int32_t* row_adapter; // [M]
     float* part;                // [S][M][r]
-    const float* base;          // [slices][M][N]
     void* C;
-    int M, K, N, r, L, S, slices;
+    int M, K, N, r, L, S;
 };
 
 // Row `lane` of a block of up to 32 rows from row m0: its adapter (-1: none), the lanes that share it,
@@ -142,126 +139,6 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const Lora
         }
         __syncthreads();
     }
-    }
-}
-
-__host__ __device__ inline int lora_t_stride(int r) {   // elements between rows of T's hi (or lo) tile
-    const int bytes = ((r + 15) / 16) * 32;
-    return (bytes % 64 == 0 ? bytes + 32 : bytes) / 2;    // 32 mod 64: the lanes' 8-byte reads miss no bank
-}
-
-// The second product of up to 16 rows: blockIdx.y is a row, the CTA takes all rows that share its
-// adapter when it is the first of them, and 256 channels. MMA rows are rows of C, MMA columns channels:
-// column c of tile j is channel 8 (c / 2) + 2 j + c % 2 of the warp's 32, so a lane's four tiles are
-// eight consecutive channels of C.
-template <typename T>
-__global__ void __launch_bounds__(kLoraThreads) lora_expand_kernel(const LoraParams p) {
-    extern __shared__ __align__(16) uint8_t lora_smem[];
-    __shared__ int list[16];
-    __shared__ float up[16];
-    using Ops = GsOps<T>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int ts = lora_t_stride(p.r), r16 = (p.r + 15) / 16;
-    T* thi = reinterpret_cast<T*>(lora_smem);
-    T* tlo = thi + (size_t)16 * ts;
-    pdl_wait();
-    pdl_trigger();
-    const LoraBlock blk(p, 0, 16);
-    const int i = blockIdx.y;
-    const int adapter = __shfl_sync(0xffffffffu, blk.adapter, i);
-    const unsigned same = __shfl_sync(0xffffffffu, blk.peers, i) & ((1u << p.M) - 1u);
-    if (__ffs(same) - 1 != i) return;
-    const int n = __popc(same);
-    if (threadIdx.x < 32 && ((same >> lane) & 1u)) list[__popc(same & ((1u << lane) - 1u))] = lane;
-    __syncthreads();
-    const bool low = adapter >= 0;
-    if (low) {
-        // row m of T: the slices' sums in order, times the adapter's scale; a warp per row
-        const float sc = __ldg(p.scale + adapter);
-        for (int m = warp; m < 16; m += kLoraWarps) {
-            float big = 0.0f, v[8];   // r <= 256
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int j = lane + 32 * q;
-                v[q] = 0.0f;
-                if (m < n && j < p.r) {
-                    const float* at = p.part + (size_t)list[m] * p.r + j;
-                    float s = 0.0f;
-#pragma unroll 4
-                    for (int k = 0; k < p.S; ++k) s += __ldcg(at + (size_t)k * p.M * p.r);
-                    v[q] = s * sc;
-                    big = fmaxf(big, fabsf(v[q]));
-                }
-            }
-            const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(big));
-            const int e = top ? min(max((int)(top >> 23) - 127 - 14, -100), 100) : 0;
-            const float down = __int_as_float((127 - e) << 23);
-            if (lane == 0) up[m] = __int_as_float((127 + e) << 23);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const int j = lane + 32 * q;
-                if (j < 16 * r16) {
-                    const float x = v[q] * down;
-                    const T h = Act<T>::from_f32(x);
-                    thi[m * ts + j] = h;
-                    tlo[m * ts + j] = Act<T>::from_f32(x - Act<T>::to_f32(h));
-                }
-            }
-        }
-        __syncthreads();
-    }
-    const T* Lb = static_cast<const T*>(p.Lb) + (low ? (size_t)adapter * p.N * p.r : 0);
-    T* C = static_cast<T*>(p.C);
-    const int n0 = blockIdx.x * 256 + 32 * warp;
-    if (n0 >= p.N) return;   // (N is a multiple of 128: a warp's 32 channels are all there or none)
-    float acc[4][4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.0f;
-    if (low) {
-        const T* brow = Lb + (size_t)(n0 + 8 * (g >> 1) + (g & 1)) * p.r + 4 * t;
-#pragma unroll 4
-        for (int q = 0; q < r16; ++q) {
-            uint2 bv[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                bv[j] = 16 * q + 4 * t < p.r ? __ldg(reinterpret_cast<const uint2*>(brow + (size_t)(2 * j) * p.r + 16 * q))
-                                             : make_uint2(0, 0);
-            const T* th = thi + g * ts + 16 * q + 4 * t;
-            const T* tl = tlo + g * ts + 16 * q + 4 * t;
-            const uint2 h0 = *reinterpret_cast<const uint2*>(th), h1 = *reinterpret_cast<const uint2*>(th + 8 * ts);
-            const uint2 l0 = *reinterpret_cast<const uint2*>(tl), l1 = *reinterpret_cast<const uint2*>(tl + 8 * ts);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                Ops::mma(acc[j], h0.x, h1.x, h0.y, h1.y, bv[j].x, bv[j].y);
-                Ops::mma(acc[j], l0.x, l1.x, l0.y, l1.y, bv[j].x, bv[j].y);
-            }
-        }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {   // rows g and g + 8
-        const int m = 8 * h + g;
-        if (m >= n) continue;
-        const size_t at = (size_t)list[m] * p.N + n0 + 8 * t;
-        float y[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int s = 0; s < p.slices; ++s) {
-            const float4* q = reinterpret_cast<const float4*>(p.base + (size_t)s * p.M * p.N + at);
-            const float4 u = __ldcg(q), v = __ldcg(q + 1);
-            y[0] += u.x; y[1] += u.y; y[2] += u.z; y[3] += u.w;
-            y[4] += v.x; y[5] += v.y; y[6] += v.z; y[7] += v.w;
-        }
-        if (low) {
-            const float f = up[m];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                y[2 * j] = fmaf(acc[j][2 * h], f, y[2 * j]);
-                y[2 * j + 1] = fmaf(acc[j][2 * h + 1], f, y[2 * j + 1]);
-            }
-        }
-        uint4 o;
-        T* oh = reinterpret_cast<T*>(&o);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) oh[i] = Act<T>::from_f32(y[i]);
-        *reinterpret_cast<uint4*>(C + at) = o;
     }
 }
 
@@ -381,21 +258,22 @@ int lora_sm_count() {
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct LoraGemvPlan {
-    int S, slices;
-    size_t off_y, off_part, total;
+    int S;
+    size_t off_part, total;
 };
 
 LoraGemvPlan plan_lora_gemv(int M, int N, int K, int group, int rank) {
     LoraGemvPlan pl = {};
-    const GemvStreamPlan q = plan_gemv_stream(M, N, K, group, 0, lora_sm_count());
+    const GemvStreamPlan q = plan_gemv_lora(M, N, K, group, 0, lora_sm_count(), rank);
     if (!q.ok) return pl;
-    pl.slices = q.slices;
-    pl.S = shrink_slices(M, K, 16, lora_sm_count());
-    pl.off_y = up256(kGemvStreamCounterBytes + q.partial_bytes);
-    pl.off_part = pl.off_y + up256((size_t)pl.slices * M * N * 4);
+    pl.S = shrink_slices(M, K, 8, lora_sm_count());
+    pl.off_part = up256(kGemvStreamCounterBytes + q.partial_bytes);
     pl.total = pl.off_part + up256((size_t)pl.S * M * rank * 4);
     return pl;
 }
+
+// The decode kernel takes up to 8 rows, and two values of t per thread.
+bool lora_gemv_fits(int M, int rank) { return M <= 8 && M * rank <= 1024; }
 
 struct LoraTcPlan {
     int rows;        // rows of A taken at a time
@@ -440,19 +318,18 @@ cudaError_t launch_shrink(const LoraParams& p, int shares, cudaStream_t stream) 
 template <typename T>
 int launch_lora_gemv(LoraParams p, const LoraGemvPlan& pl, uint8_t* ws, const void* tiled, int group, int sym, int dtype,
                      int* dev_status, cudaStream_t stream) {
-    float* y = reinterpret_cast<float*>(ws + pl.off_y);
     p.S = pl.S;
     p.part = reinterpret_cast<float*>(ws + pl.off_part);
-    p.base = y;
-    const dim3 block(kLoraThreads);
-    const cudaError_t e = p.M <= 8 ? launch_shrink<1, T>(p, p.M, stream) : launch_shrink<2, T>(p, p.M, stream);
-    if (e != cudaSuccess) return W4A16_ECUDA;
-    const int st = launch_gemv_stream_f32(p.A, dtype, p.M, p.K, tiled, p.N, group, sym, y, &p.slices, ws, dev_status, stream);
-    if (st != W4A16_OK) return st;
-    const size_t smem = (size_t)2 * 16 * lora_t_stride(p.r) * 2;
-    return launch_pdl(lora_expand_kernel<T>, dim3((p.N + 255) / 256, p.M), block, smem, stream, p) == cudaSuccess
-               ? W4A16_OK
-               : W4A16_ECUDA;
+    if (launch_shrink<1, T>(p, p.M, stream) != cudaSuccess) return W4A16_ECUDA;
+    GemvLora lora = {};
+    lora.b = p.Lb;
+    lora.scale = p.scale;
+    lora.row_adapter = p.row_adapter;
+    lora.part = p.part;
+    lora.slices = pl.S;
+    lora.rank = p.r;
+    lora.adapters = p.L;
+    return launch_gemv_lora(p.A, dtype, p.M, p.K, tiled, p.N, group, sym, p.C, lora, ws, dev_status, stream);
 }
 
 // One piece of rows on the tensor cores. `pl` is the whole batch's plan: its offsets, bn and widths
@@ -500,7 +377,7 @@ size_t lora_workspace_bytes(int M, int N, int K, int group, int rank, int adapte
     // the larger need over both types and both forms, so that a forced kernel also fits
     const size_t a = plan_lora_tc(M, K, rank, adapters, 2).total, b = plan_lora_tc(M, K, rank, adapters, 4).total;
     const size_t tc = a > b ? a : b;
-    const size_t gemv = M <= 16 ? plan_lora_gemv(M, N, K, group, rank).total : 0;
+    const size_t gemv = lora_gemv_fits(M, rank) ? plan_lora_gemv(M, N, K, group, rank).total : 0;
     return tc > gemv ? tc : gemv;
 }
 
@@ -521,7 +398,7 @@ int launch_lora_gemm(const void* A, int a_dtype, int M, int K, const void* tiled
     p.N = N;
     p.r = rank;
     p.L = adapters;
-    if (M <= 16 && w4a16_select_kernel(M, N, K, group) == W4A16_KERNEL_GEMV) {
+    if (lora_gemv_fits(M, rank) && w4a16_select_kernel(M, N, K, group) == W4A16_KERNEL_GEMV) {
         const LoraGemvPlan pl = plan_lora_gemv(M, N, K, group, rank);
         if (pl.total)
             return bf16 ? launch_lora_gemv<__nv_bfloat16>(p, pl, ws, tiled, group, sym, a_dtype, dev_status, stream)

@@ -45,10 +45,17 @@ int launch_moe_gemv(const void* A, int a_dtype, int R, int K, const void* tiled,
 int launch_moe_gemm(const void* A, int a_dtype, int R, int K, const void* tiled, int E, const int32_t* offsets, int N,
                     int group, int sym, void* C, void* workspace, int kernel, int* dev_status, cudaStream_t stream);
 
-// The dense decode kernel with FP32 outputs y [slices][M][N] (to be added up) for a kernel that adds to
-// the layer's output before it is rounded. `workspace` under the contract of w4a16_gemm.
-int launch_gemv_stream_f32(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
-                           float* y, int* slices, void* workspace, int* dev_status, cudaStream_t stream);
+// The dense decode kernel with low-rank terms added to its FP32 sums (gemv_stream.cu).
+struct GemvLora {
+    const void* b;              // Lb [adapters][N][rank]
+    const float* scale;         // [adapters]
+    const int32_t* row_adapter; // [M]
+    const float* part;          // [slices][M][rank]: A . La^T over slices of K
+    int slices, rank, adapters;
+};
+GemvStreamPlan plan_gemv_lora(int M, int N, int K, int group, int sym, int n_sm, int rank);
+int launch_gemv_lora(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym, void* C,
+                     const GemvLora& lora, void* workspace, int* dev_status, cudaStream_t stream);
 
 // The layer with low-rank adapters.
 constexpr int kLoraMaxRank = 256;
