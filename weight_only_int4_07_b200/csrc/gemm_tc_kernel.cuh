@@ -444,7 +444,13 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 if (u0 < u1) gw.init(run_tab, blk_tab, p.E, p.N / 128, u0 / UT);
             if constexpr (US) {
                 // each own unit into accumulator ab * kIss + j (two per issuer, alternating)
+                long long low_from = kLora ? u0 - lw.ku + UT : 0, tile_to = kLora ? u0 - lw.ku + lw.len : 0;
                 for (long long i = u0; i < u1; ++i) {
+                    if (kLora && i == tile_to) {
+                        lw.step(lw.len - lw.ku);
+                        low_from = i + UT;
+                        tile_to = i + lw.len;
+                    }
                     if (kIss == 1 || (int)((i - u0) & 1) == j) {
                         const int slot = ab * kIss + j;
                         if (!mbar_wait(&accempty[slot], ((uint32_t)use[ab] & 1u) ^ 1u, abort_flag, p.dev_status,
@@ -456,7 +462,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         const uint32_t d_tmem = tmem + (uint32_t)(slot * kCols);
                         const uint32_t a_tm = tmem_w + (uint32_t)(s * kTcStepCols);
                         const uint32_t b_sm = smem_u32(ring_a + (size_t)s * kSlotA);
-                        const uint32_t ids = kLora && lw.low() ? idesc_low : idesc;
+                        const uint32_t ids = kLora && i >= low_from ? idesc_low : idesc;
                         mma4_f16_ts(d_tmem, a_tm, smem_desc_sw128(b_sm), ids, 0u);
                         mma4_f16_ts(d_tmem, a_tm + 32u, smem_desc_sw128(b_sm + kSlotA / 2), ids, 1u);
                         mma_commit(&free_s[s]);
@@ -464,7 +470,6 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         ++use[ab];
                         ab ^= 1;
                     }
-                    if constexpr (kLora) lw.step(1);
                     if (++s == NS) {
                         s = 0;
                         ph ^= 1u;
@@ -476,6 +481,8 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 const long long tau = kLora ? 0 : i / UT;
                 const long long tile_end = kLora ? i + (lw.len - lw.ku) : (tau + 1) * UT;
                 const long long seg_end = u1 < tile_end ? u1 : tile_end;
+                const long long low_from = kLora ? i - lw.ku + UT : 0;
+                if constexpr (kLora) lw.step((int)(seg_end - i));
                 uint32_t idesc_t = idesc;
                 if constexpr (kGrp && BN > 64) {   // as many columns as the tile has rows, in boxes
                     if (i > u0) gw.next();
@@ -499,13 +506,12 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         // from the two 64-K boxes of the step's tile; one commit frees both tiles
                         const uint32_t a_tm = tmem_w + (uint32_t)(s * kTcStepCols);
                         const uint32_t b_sm = smem_u32(ring_a + (size_t)s * kSlotA);
-                        const uint32_t ids = kLora && lw.low() ? idesc_low : idesc_t;
+                        const uint32_t ids = kLora && i >= low_from ? idesc_low : idesc_t;
                         mma4_f16_ts(d_tmem, a_tm, smem_desc_sw128(b_sm), ids, first ? 0u : 1u);
                         mma4_f16_ts(d_tmem, a_tm + 32u, smem_desc_sw128(b_sm + kSlotA / 2), ids, 1u);
                         mma_commit(&free_s[s]);
                         first = false;
                     }
-                    if constexpr (kLora) lw.step(1);
                     if (++s == NS) {
                         s = 0;
                         ph ^= 1u;
@@ -827,22 +833,35 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             b0 = __ldg(src);
             if (j + 8 < p.rank) b1 = __ldg(src + 1);
         };
+        // (a tile's weight units run to `tend` by the dense loop; the walk moves per tile and low-rank unit)
         if constexpr (kLora) {
             lw.init(cum_tab, UT, p.mblocks, u0);
+            tend = lw.low() ? u0 : u0 + (UT - lw.ku);
             if (u0 < u1 && lw.len > UT) {
                 piece = piece_of(lw.low() ? lw.ku - UT : 0);
                 if (lw.low()) {
                     fetch();
                     if (lw.ku + 1 < lw.len) piece = piece_of(lw.ku + 1 - UT);
+                } else {
+                    lw.ku = UT;
                 }
+            } else {
+                lw.ku = UT;
             }
         }
         for (long long i = u0; i < u1 && ok;) {
             if constexpr (kLora) {
-                if (lw.low()) {
+                if (i == tend) {
+                    if (lw.ku == lw.len) {   // the next tile's weight units
+                        lw.step(0);
+                        lw.ku = UT;
+                        tend = i + UT;
+                        if (lw.len > UT) piece = piece_of(0);
+                        continue;
+                    }
                     // bf16 layer: [Lb | Lb] beside T's [hi | lo]; fp16 layer: Lb = hi + lo exactly (8 + 3
                     // bits), blocks [hi | hi], [lo | 0] beside T's [hi | lo], [hi | 0]
-                    if (!tc_wait(&free_s[s], ph ^ 1u, abort_flag, p.dev_status, p.wait_ns)) {
+                    if (!tc_wait(&free_s[s], ph ^ 1u, abort_flag, p.dev_status, wait_ns)) {
                         ok = false;
                         break;
                     }
@@ -877,15 +896,10 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                             out[8 + c] = blk & 1 ? 0u : hi;
                         }
                     }
-                    lw.step(1);
-                    ++i;
-                    if (i < u1 && lw.len > UT) {
-                        if (lw.low()) {
-                            fetch();
-                            if (lw.ku + 1 < lw.len) piece = piece_of(lw.ku + 1 - UT);
-                        } else {
-                            piece = piece_of(0);
-                        }
+                    tend = ++i;
+                    if (++lw.ku < lw.len) {
+                        fetch();
+                        if (lw.ku + 1 < lw.len) piece = piece_of(lw.ku + 1 - UT);
                     }
                     tmem_st16(d_lane + (uint32_t)(s * kTcStepCols), out);
                     tmem_st_wait();
@@ -898,22 +912,14 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     }
                     continue;
                 }
-                tend = i + (UT - lw.ku);
             }
             const long long seg_end = u1 < tend ? u1 : tend;
             const int nu = (int)(seg_end - i < kUPL ? seg_end - i : kUPL);
             i += nu;
             if constexpr (kLora) {
-                const bool last = lw.ku + nu == UT && lw.len > UT;   // the low-rank units come next
-                lw.ku += nu;
-                if (last) {
+                if (i == tend && lw.len > UT) {   // the tile's low-rank units come next
                     fetch();
                     if (lw.len > UT + 1) piece = piece_of(1);
-                }
-                if (lw.ku == lw.len) {
-                    lw.ku -= nu;
-                    lw.step(nu);
-                    if (i < u1 && lw.len > UT) piece = piece_of(0);
                 }
             } else if (i == tend) {
                 tend += UT;
