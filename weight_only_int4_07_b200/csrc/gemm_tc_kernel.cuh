@@ -177,8 +177,8 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile
 // lora_place_kernel) holds, for every adapter of the row block, its rows' rank products as hi + lo and
 // zeros in the other rows. cum: low-rank units before each row block.
 struct TcLoraWalk {
-    const int* cum;
-    int UT, mblocks, nt, mb, ku, len;
+    const int* cum = nullptr;
+    int UT = 0, mblocks = 0, nt = 0, mb = 0, ku = 0, len = 0;
     __device__ __forceinline__ void init(const int* c, int units, int blocks, long long u) {
         cum = c;
         UT = units;
@@ -276,8 +276,10 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         tmem_relinquish();
     }
     if constexpr (MODE != kTcDense) {
-        // (launched as a programmatic dependent: what it reads may be the previous kernel's)
-        pdl_wait();
+        // (launched as a programmatic dependent: what it reads may be the previous kernel's. kTcLora: that one
+        // only places T, which the activation loader waits for by itself; it lets this one start after
+        // everything before it has completed.)
+        if (!kLora) pdl_wait();
         pdl_trigger();
     }
     if constexpr (kGrp) {
@@ -385,6 +387,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             int ku = (int)(u0 - tau0 * UT), mb = kGrp ? 0 : (int)(tau0 % p.mblocks);
             MoeWalk gw;
             TcLoraWalk lw;
+            bool placed = false;
             if constexpr (kGrp) gw.init(run_tab, blk_tab, p.E, p.N / 128, tau0);
             if constexpr (kLora) lw.init(cum_tab, UT, p.mblocks, u0);
             for (long long i = u0; i < u1; ++i) {
@@ -398,6 +401,10 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 // (a grouped tile may run into the next expert's rows: those columns are not stored)
                 const int row = kGrp ? gw.row0(BN) : (kLora ? lw.mb : mb) * BN;
                 const bool low = kLora && lw.low();
+                if (low && !placed) {
+                    pdl_wait();
+                    placed = true;
+                }
                 const CUtensorMap* map = low ? &tmT : &tmA;
                 const int kx = kLora ? (low ? lw.ku - UT : lw.ku) : ku;
                 if (!mbar_wait(&free_s[s], ph ^ 1u, abort_flag, p.dev_status, wait_ns)) break;
@@ -424,6 +431,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             volatile int keep = 0;
             for (int q = 0; q < NS; ++q)
                 if (issued[q] > 0) mbar_wait(&full_a[q], (uint32_t)(issued[q] - 1) & 1u, &keep, nullptr, kTcDrainNs);
+            if (kLora) pdl_wait();   // this kernel does not complete before the one that it overtook
         }
     } else if (warp >= kTcWarpMma && warp < kTcWarpMma + kIss) {
         // ------------------------------------------------------------ MMA issuers

@@ -36,6 +36,10 @@ struct LoraParams {
     const float* scale;         // [L]
     const int32_t* row_adapter; // [M]
     float* part;                // [S][M][r]
+    int* units;                 // tensor cores: the row blocks' low-rank units and pieces (null: none wanted)
+    int* pieces;
+    int* bad;
+    int bn, max_units, per;
     void* C;
     int M, K, N, r, L, S;
 };
@@ -54,9 +58,74 @@ struct LoraBlock {
     }
 };
 
+// slot[a]: place of adapter a among the adapters of the bn rows from m0, for those that are there. Four
+// adapters per thread: f, their flags, and `before`, the first one's place. Returns how many there are.
+__device__ __forceinline__ int lora_slots(const LoraParams& p, int m0, int bn, int* slot, int* wsum, int (&f)[4], int& before) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    for (int a = tid; a < p.L; a += kLoraThreads) slot[a] = 0;
+    __syncthreads();
+    for (int i = tid; i < bn && m0 + i < p.M; i += kLoraThreads) {
+        const int a = p.row_adapter[m0 + i];
+        if ((unsigned)a < (unsigned)p.L) slot[a] = 1;
+    }
+    __syncthreads();
+    int c = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        f[q] = 4 * tid + q < p.L ? slot[4 * tid + q] : 0;
+        c += f[q];
+    }
+    int x = c;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) wsum[warp] = x;
+    __syncthreads();
+    before = x - c;
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < kLoraWarps; ++w) {
+        if (w < warp) before += wsum[w];
+        total += wsum[w];
+    }
+    int at = before;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (4 * tid + q < p.L) {
+            slot[4 * tid + q] = at;
+            at += f[q];
+        }
+    __syncthreads();
+    return total;
+}
+
+// The low-rank units and pieces of row block mb, and the flag of values that are not finite.
+__device__ __forceinline__ void lora_list(const LoraParams& p, int mb) {
+    __shared__ int slot[kRouteMaxBins];
+    __shared__ int wsum[kLoraWarps];
+    int f[4], before;
+    const int total = lora_slots(p, mb * p.bn, p.bn, slot, wsum, f, before);
+    const int pr = (p.r + 15) / 16, lu = (total * pr + p.per - 1) / p.per;
+    int* pieces = p.pieces + (size_t)mb * p.max_units * p.per;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (f[q]) {
+            for (int j = 0; j < pr; ++j) pieces[before * pr + j] = 256 * (4 * threadIdx.x + q) + j;
+            ++before;
+        }
+    for (int j = total * pr + threadIdx.x; j < lu * p.per; j += kLoraThreads) pieces[j] = -1;
+    if (threadIdx.x == 0) {
+        p.units[mb] = lu;
+        if (mb == 0) *p.bad = 0;
+    }
+}
+
 // T's partial sums over one slice of K (blockIdx.x) for a block of 8 NB rows (blockIdx.y); the adapters
 // of the block are dealt out to gridDim.z CTAs. Warp w takes every eighth 32-K step of the slice; MMA
-// rows are ranks, MMA columns the adapter's rows.
+// rows are ranks, MMA columns the adapter's rows. With p.units, one more CTA per row block of bn rows
+// (blockIdx.z = gridDim.z - 1) lists its units.
 // RB: 16-rank blocks of one pass over K.
 template <int NB, int RB, typename T>
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const LoraParams p) {
@@ -66,9 +135,15 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const Lora
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     pdl_wait();
     pdl_trigger();
+    int shares = gridDim.z;
+    if (p.units && blockIdx.z == --shares) {
+        if (blockIdx.x == 0 && blockIdx.y * 8 * NB % p.bn == 0) lora_list(p, blockIdx.y * 8 * NB / p.bn);
+        // (bn below a block's rows: one row block)
+        return;
+    }
     const LoraBlock blk(p, blockIdx.y * 8 * NB, 8 * NB);
     const int here = __popc(blk.firsts);
-    for (int nth = blockIdx.z; nth < here; nth += gridDim.z) {
+    for (int nth = blockIdx.z; nth < here; nth += shares) {
     unsigned left = blk.firsts;
     for (int q = 0; q < nth; ++q) left &= left - 1;
     const int first = __ffs(left) - 1;
@@ -145,65 +220,20 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const Lora
 // T as the tensor-core layer takes it. A row block (bn rows) has its adapters in order, each with
 // pr = ceil(r / 16) pieces of 16 ranks, `per` pieces (4 in a bf16 layer, 2 in an fp16 one) to a low-rank
 // unit of 128 columns: per piece [hi | lo] (bf16), or [hi | lo | hi | 0] (fp16, whose Lb is split into hi and
-// lo too). A warp writes one row, all units of its block; the block's first CTA lists units and pieces.
+// lo too). A warp writes one row, all units of its block.
 template <typename T>
-__global__ void __launch_bounds__(kLoraThreads) lora_place_kernel(const LoraParams p, int bn, int max_units,
-                                                                  __nv_bfloat16* __restrict__ placed,
-                                                                  int* __restrict__ units, int* __restrict__ pieces,
-                                                                  int* __restrict__ bad) {
+__global__ void __launch_bounds__(kLoraThreads) lora_place_kernel(const LoraParams p, __nv_bfloat16* __restrict__ placed) {
     constexpr int kPer = std::is_same<T, __nv_bfloat16>::value ? 4 : 2;
     __shared__ int slot[kRouteMaxBins];
     __shared__ int wsum[kLoraWarps];
     __shared__ __align__(16) __nv_bfloat16 hi[kLoraWarps][kLoraMaxRank], lo[kLoraWarps][kLoraMaxRank];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int row = blockIdx.x * kLoraWarps + warp, mb = blockIdx.x * kLoraWarps / bn, m0 = mb * bn;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int row = blockIdx.x * kLoraWarps + warp, m0 = blockIdx.x * kLoraWarps / p.bn * p.bn;
     const int pr = (p.r + 15) / 16;
-    for (int a = tid; a < p.L; a += kLoraThreads) slot[a] = 0;
-    __syncthreads();
     pdl_wait();
     pdl_trigger();
-    for (int i = tid; i < bn && m0 + i < p.M; i += kLoraThreads) {
-        const int a = p.row_adapter[m0 + i];
-        if ((unsigned)a < (unsigned)p.L) slot[a] = 1;
-    }
-    __syncthreads();
-    // slot[a]: the adapter's place among the block's, four adapters per thread
-    int f[4], c = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        f[q] = 4 * tid + q < p.L ? slot[4 * tid + q] : 0;
-        c += f[q];
-    }
-    int x = c;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-    }
-    if (lane == 31) wsum[warp] = x;
-    __syncthreads();
-    int before = x - c, total = 0;
-#pragma unroll
-    for (int w = 0; w < kLoraWarps; ++w) {
-        if (w < warp) before += wsum[w];
-        total += wsum[w];
-    }
-    const bool lists = blockIdx.x * kLoraWarps % bn == 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-        if (4 * tid + q < p.L) {
-            slot[4 * tid + q] = before;
-            if (lists && f[q])
-                for (int j = 0; j < pr; ++j) pieces[(size_t)mb * max_units * kPer + before * pr + j] = 256 * (4 * tid + q) + j;
-            before += f[q];
-        }
-    const int lu = (total * pr + kPer - 1) / kPer;
-    if (lists) {
-        for (int j = total * pr + tid; j < lu * kPer; j += kLoraThreads) pieces[(size_t)mb * max_units * kPer + j] = -1;
-        if (tid == 0) units[mb] = lu;
-        if (blockIdx.x == 0 && tid == 0) *bad = 0;
-    }
-    __syncthreads();
+    int f[4], before;
+    const int lu = (lora_slots(p, m0, p.bn, slot, wsum, f, before) * pr + kPer - 1) / kPer;
     if (row >= p.M) return;
     int a = p.row_adapter[row];
     if ((unsigned)a >= (unsigned)p.L) a = -1;
@@ -213,6 +243,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_place_kernel(const LoraPara
         for (int j = lane; j < 16 * pr; j += 32) {
             float s = 0.0f;
             if (j < p.r)
+#pragma unroll 8
                 for (int k = 0; k < p.S; ++k) s += __ldcg(p.part + ((size_t)k * p.M + row) * p.r + j);
             s *= sc;
             const __nv_bfloat16 h = __float2bfloat16_rn(s);
@@ -221,7 +252,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_place_kernel(const LoraPara
         }
     }
     __syncwarp();
-    uint4* out = reinterpret_cast<uint4*>(placed + (size_t)row * max_units * 128);
+    uint4* out = reinterpret_cast<uint4*>(placed + (size_t)row * p.max_units * 128);
     for (int q = lane; q < lu * 16; q += 32) {   // 8 columns: unit q / 16, block (q / 4) % 4, part q % 4
         const int b = (q >> 2) & 3, part = q & 3;
         const int piece = (q >> 4) * kPer + (kPer == 4 ? b : b >> 1);
@@ -238,7 +269,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_place_kernel(const LoraPara
 // K slices of the shrink kernel: about two CTAs per SM when rows share adapters, a 32-K step per warp.
 int shrink_slices(int M, int K, int rows, int n_sm) {
     int S = 2 * n_sm / ((M + rows - 1) / rows);
-    if (S > 16) S = 16;
+    if (S > 32) S = 32;
     if (S > K / 256) S = K / 256;
     return S < 1 ? 1 : S;
 }
@@ -297,7 +328,7 @@ LoraTcPlan plan_lora_tc(int M, int K, int rank, int adapters, int per) {
     pl.off_part = up256(kGemvStreamCounterBytes + (size_t)lora_sm_count() * pl.bn * 128 * sizeof(float));
     // S M of any piece: one slice of up to `rows` rows, or at most two CTAs per SM of 32 rows each
     size_t sm = (size_t)64 * lora_sm_count();
-    if (sm > (size_t)16 * pl.rows) sm = (size_t)16 * pl.rows;
+    if (sm > (size_t)32 * pl.rows) sm = (size_t)32 * pl.rows;
     if (sm < (size_t)pl.rows) sm = (size_t)pl.rows;
     pl.off_placed = pl.off_part + up256(sm * rank * 4);
     pl.off_units = pl.off_placed + up256((size_t)pl.rows * pl.max_units * 256);
@@ -309,7 +340,7 @@ LoraTcPlan plan_lora_tc(int M, int K, int rank, int adapters, int per) {
 
 template <int NB, typename T>
 cudaError_t launch_shrink(const LoraParams& p, int shares, cudaStream_t stream) {
-    const dim3 grid(p.S, (p.M + 8 * NB - 1) / (8 * NB), shares), block(kLoraThreads);
+    const dim3 grid(p.S, (p.M + 8 * NB - 1) / (8 * NB), shares + (p.units ? 1 : 0)), block(kLoraThreads);
     if (p.r <= 16) return launch_pdl(lora_shrink_kernel<NB, 1, T>, grid, block, 0, stream, p);
     if (p.r <= 32) return launch_pdl(lora_shrink_kernel<NB, 2, T>, grid, block, 0, stream, p);
     return launch_pdl(lora_shrink_kernel<NB, 4, T>, grid, block, 0, stream, p);
@@ -344,13 +375,15 @@ int launch_lora_tc(LoraParams p, const LoraTcPlan& pl, uint8_t* ws, const void* 
     p.S = shrink_slices(p.M, p.K, 32, n_sm);
     p.part = reinterpret_cast<float*>(ws + pl.off_part);
     __nv_bfloat16* placed = reinterpret_cast<__nv_bfloat16*>(ws + pl.off_placed);
-    int* units = reinterpret_cast<int*>(ws + pl.off_units);
-    int* pieces = reinterpret_cast<int*>(ws + pl.off_pieces);
-    int* bad = reinterpret_cast<int*>(ws + pl.off_bad);
-    const dim3 block(kLoraThreads);
+    p.units = reinterpret_cast<int*>(ws + pl.off_units);
+    p.pieces = reinterpret_cast<int*>(ws + pl.off_pieces);
+    p.bad = reinterpret_cast<int*>(ws + pl.off_bad);
+    p.bn = pl.bn;
+    p.max_units = pl.max_units;
+    p.per = pl.per;
     if (launch_shrink<4, T>(p, shrink_shares(p.M, p.S, 32, n_sm), stream) != cudaSuccess) return W4A16_ECUDA;
-    if (launch_pdl(lora_place_kernel<T>, dim3((p.M + kLoraWarps - 1) / kLoraWarps), block, 0, stream, p, pl.bn, pl.max_units,
-                   placed, units, pieces, bad) != cudaSuccess)
+    if (launch_pdl(lora_place_kernel<T>, dim3((p.M + kLoraWarps - 1) / kLoraWarps), dim3(kLoraThreads), 0, stream, p,
+                   placed) != cudaSuccess)
         return W4A16_ECUDA;
     CUtensorMap map, map_t;
     if (!make_act_map(&map, p.A, p.M, p.K, pl.bn, dtype == W4A16_BF16) ||
@@ -360,11 +393,11 @@ int launch_lora_tc(LoraParams p, const LoraTcPlan& pl, uint8_t* ws, const void* 
     prm.mblocks = mblocks;
     prm.C = p.C;
     prm.off_grp = tp.off_bar + 1024;
-    prm.lora_units = units;
-    prm.lora_pieces = pieces;
+    prm.lora_units = p.units;
+    prm.lora_pieces = p.pieces;
     prm.lora_b = p.Lb;
     prm.row_adapter = p.row_adapter;
-    prm.lora_bad = bad;
+    prm.lora_bad = p.bad;
     prm.max_pieces = pl.max_units * pl.per;
     prm.rank = p.r;
     prm.adapters = p.L;
