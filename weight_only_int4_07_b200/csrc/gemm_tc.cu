@@ -2,6 +2,8 @@
 // tensor maps, shared-memory layout, dispatch on the rows of A.
 #include <cudaTypedefs.h>
 
+#include <mutex>
+
 #include "gemm_tc_kernel.cuh"
 #include "routed.cuh"
 

@@ -60,7 +60,6 @@
 // the MMA thread waits for its last MMAs, and the CTA frees its tensor memory and returns.
 #pragma once
 
-#include <mutex>
 #include <type_traits>
 
 #include "common.cuh"
@@ -1064,13 +1063,8 @@ inline TcParams tc_params(const TcPlan& pl, const void* tiled, int M, int N, int
 
 template <int BN, typename T, bool US, int MODE>
 int launch_tc_typed(const CUtensorMap& map, const CUtensorMap& map_t, const TcParams& prm, size_t smem, cudaStream_t stream) {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(tc_gemm_kernel<BN, T, US, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kTcSmemMax);
-    });
-    if (attr_err != cudaSuccess) return W4A16_ECUDA;
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(tc_gemm_kernel<BN, T, US, MODE>, kTcSmemMax, done)) return W4A16_ECUDA;
     if constexpr (MODE != kTcDense)
         return launch_pdl(tc_gemm_kernel<BN, T, US, MODE>, dim3(prm.P), dim3(kTcThreads), smem, stream, map, map_t, prm) ==
                        cudaSuccess

@@ -47,11 +47,11 @@
 // Every wait is bounded (the limit of w4a16_set_wait_limit_ns, 2 s by default); on expiry the
 // kernel records W4A16_ETIMEOUT, stops issuing copies, still passes every barrier and tile
 // counter, and lets the copies in flight land before it exits.
-#include <mutex>
 #include <type_traits>
 
 #include "common.cuh"
 #include "dequant.cuh"
+#include "pdl.cuh"
 #include "routed.cuh"
 #include "sm100_ptx.cuh"
 #include "tiled_layout.cuh"
@@ -840,13 +840,8 @@ __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(c
 
 template <int NB, typename T, int GROUP, bool ODD, bool SL, bool LO>
 int launch_typed(const GsParams& prm, size_t smem, cudaStream_t stream) {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(gemv_stream_kernel<NB, T, GROUP, ODD, SL, LO>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kGsSmemMax);
-    });
-    if (attr_err != cudaSuccess) return W4A16_ECUDA;
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(gemv_stream_kernel<NB, T, GROUP, ODD, SL, LO>, kGsSmemMax, done)) return W4A16_ECUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(prm.P * prm.slices, 1, 1);
     cfg.blockDim = dim3(kGsThreads, 1, 1);

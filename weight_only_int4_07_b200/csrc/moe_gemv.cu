@@ -23,7 +23,6 @@
 // Columns of an MMA past the tile's rows hold whatever the shared memory held; columns are
 // independent and those are not stored.
 // Every wait is bounded as in gemv_stream.cu.
-#include <mutex>
 #include <type_traits>
 
 #include "dequant.cuh"
@@ -542,12 +541,8 @@ MgPlan plan_moe_gemv(int R, int E, int N, int K, int group, int sym) {
 
 template <typename T, int GROUP>
 int launch_mg(const MgParams& prm, size_t smem, cudaStream_t stream) {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(moe_gemv_kernel<T, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMgSmemMax);
-    });
-    if (attr_err != cudaSuccess) return W4A16_ECUDA;
+    static std::atomic<uint64_t> done{0};
+    if (!allow_smem(moe_gemv_kernel<T, GROUP>, kMgSmemMax, done)) return W4A16_ECUDA;
     return launch_pdl(moe_gemv_kernel<T, GROUP>, dim3(prm.P), dim3(kMgThreads), smem, stream, prm) == cudaSuccess
                ? W4A16_OK
                : W4A16_ECUDA;

@@ -3,8 +3,24 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
 
 namespace w4a16 {
+
+// Up to `bytes` of dynamic shared memory for `kernel` on the current device; `done`: the devices (by bit)
+// that know already, one word per kernel.
+template <typename F>
+inline bool allow_smem(F* kernel, size_t bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
 
 // All kernels before this one on the stream have completed and their writes are visible. A kernel
 // launched with launch_pdl runs it before it touches any buffer that another kernel may use.

@@ -324,6 +324,9 @@ def w4a16_gemm_noalloc(A, codes, scales, zeros, N, group, sym, C=None):
 
 
 # ----------------------------------------------------------------------------- routed layers
+_calls = {}
+
+
 def _need(fn, ok):
     if not ok:
         raise W4A16Error(fn, EINVAL)
@@ -352,17 +355,15 @@ def _room(fn, t, nbytes, dev, zeroed=False):
     return t
 
 
-def _raw_stream(dev):
-    """The current stream of device `dev` as a cudaStream_t (torch.cuda.current_stream builds a Python
-    object on the way, 3 us of a small call)."""
-    return torch._C._cuda_getCurrentRawStream(dev)
-
-
 def _call(name, dev, *args):
-    """One entry point on the current stream of device `dev`, with that device current."""
-    f = getattr(lib(), name)
-    stream = _raw_stream(dev)
-    if dev == torch.cuda.current_device():
+    """One entry point on the current stream of device `dev`, with that device current. (The stream and
+    the device come from the functions below torch.cuda's own: building a Python stream object is 3 us
+    of a small call.)"""
+    f = _calls.get(name)
+    if f is None:
+        f = _calls[name] = getattr(lib(), name)
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch._C._cuda_getDevice():
         st = f(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -477,7 +478,8 @@ def w4a16_moe_gemm(A, offsets, tiled, N, group, sym, C=None, workspace=None, ker
     pw = _arg(fn, tiled, torch.uint8, (E, w4a16_repack_bytes(K, N, group, sym)), dev)
     C = _out(fn, C, t, (R, N), dev)
     if workspace is None:
-        workspace = _room(fn, None, w4a16_moe_workspace_bytes(R, E, N, K, group), dev, zeroed=True)
+        with torch.cuda.device(dev):   # (the size goes by the device)
+            workspace = _room(fn, None, w4a16_moe_workspace_bytes(R, E, N, K, group), dev, zeroed=True)
     _call(fn, dev, pa, _DTYPES[t], R, K, pw, E, po, N, group, int(sym), C.data_ptr(),
           _room(fn, workspace, 0, dev).data_ptr(), workspace.numel() * workspace.element_size(), int(kernel),
           _status_arg(fn, dev_status, dev))
@@ -506,7 +508,8 @@ def w4a16_lora_gemm(A, tiled, N, group, sym, lora_a, lora_b, lora_scale, row_ada
     pr = _arg(fn, row_adapter, torch.int32, (M,), dev)
     C = _out(fn, C, t, (M, N), dev)
     if workspace is None:
-        workspace = _room(fn, None, w4a16_lora_workspace_bytes(M, N, K, group, r, L), dev, zeroed=True)
+        with torch.cuda.device(dev):   # (the size goes by the device)
+            workspace = _room(fn, None, w4a16_lora_workspace_bytes(M, N, K, group, r, L), dev, zeroed=True)
     _call(fn, dev, pa, _DTYPES[t], M, K, pw, N, group, int(sym), pla, plb, ps, L, r, pr, C.data_ptr(),
           _room(fn, workspace, 0, dev).data_ptr(), workspace.numel() * workspace.element_size(),
           _status_arg(fn, dev_status, dev))
