@@ -474,7 +474,7 @@ W4A16_API int w4a16_moe_gemm(const void* A, int a_dtype, int R, int K, const voi
  *              shared with w4a16_gemm. It holds the rank products of at most 64 MiB or 256 rows at a
  *              time, whichever is more, and of at most 16384 rows; longer batches are taken in pieces.
  *   dev_status device int or NULL: W4A16_ETIMEOUT as for w4a16_gemm.
- *   stream     cudaStream_t. Three kernel launches (each piece).
+ *   stream     cudaStream_t. Two or three kernel launches (each piece).
  * Values that are not finite: those of a row of A, of an adapter or of its scale reach only the rows that
  * use them (which are then NaN or infinite), never the other rows of the batch.
  * Ordering. No condition on the kernels before the call (the first kernel lets the layer's start only

@@ -656,7 +656,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         }
                         tc_named_bar(1, 128);
                     }
-                    if (ok && !*abort_flag) {
+                    if (__all_sync(0xffffffffu, ok && !*abort_flag)) {
 #pragma unroll
                         for (int c = 0; c < BN / 16; ++c) {
                             float y[16];
@@ -676,7 +676,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         }
                     }
                 } else {
-                    if (ok && !*abort_flag) {
+                    if (__all_sync(0xffffffffu, ok && !*abort_flag)) {
                         float* part = p.partials + (size_t)cta * BN * 128;
 #pragma unroll
                         for (int r = 0; r < BN; ++r)
@@ -766,7 +766,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     }
                     tc_named_bar(1, 128);
                 }
-                if (ok && !*abort_flag) {
+                if (__all_sync(0xffffffffu, ok && !*abort_flag)) {
                     sums([&](int c, float (&y)[16]) {
                         // the other CTAs' sums, in CTA order; the 16 loads of one CTA in flight together
 #pragma unroll 1
@@ -786,7 +786,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             } else {
                 // a later CTA of a cut tile (the tile opens its range): publish the sums and count
                 // them, without waiting
-                if (ok && !*abort_flag) {
+                if (__all_sync(0xffffffffu, ok && !*abort_flag)) {
                     float* part = p.partials + (size_t)cta * BN * 128;
                     sums([&](int c, float (&y)[16]) {
 #pragma unroll

@@ -265,14 +265,17 @@ __global__ void __launch_bounds__(kMgThreads, 1) moe_gemv_kernel(const MgParams 
     // no row of a fresh slot reads as wide
     for (int i = threadIdx.x; i < ns * 4 * MR; i += kMgThreads)
         *reinterpret_cast<uint4*>(acts + (size_t)i * kMgRowBytes + 64) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();   // (the slots are refilled by bulk copies)
     pdl_trigger();
     moe_table(p.offsets, p.E, p.R, MR, run_tab, blk_tab, [] { cta_sync(); });
     cta_sync();
 
     const long long U = (long long)blk_tab[p.E] * (N / 128) * steps;
     const int P = U < p.P ? (int)U : p.P, cta = blockIdx.x;
-    if (cta >= P) return;
-    fence_proxy_async_smem();   // (the slots written above are refilled by bulk copies)
+    if (cta >= P) {
+        pdl_wait();   // this kernel does not complete before the one that it overtook
+        return;
+    }
     const long long u0 = mg_begin(cta, U, P), u1 = mg_begin(cta + 1, U, P);
     const int nunits = (int)(u1 - u0);   // (the host keeps the units of one range below 2^31)
     const int nst = (nunits + 3) / 4;
