@@ -22,6 +22,8 @@
 // FP32 sums to the workspace and counts them (release, no wait); cf, after its own last unit,
 // waits for the count (acquire, bounded), adds the sums in CTA order, writes C and resets the
 // counter. The result does not depend on timing.
+// (Launches with adapters or experts, from 64 rows per tile: every CTA of a cut tile publishes, and
+// all of them add up a share of its rows once their ranges are done; tc_share.)
 //
 // Warp roles (768 threads):
 //   warp 0      : weight loader -- one bulk copy per two unit records (codes, scales and zeros
@@ -83,6 +85,11 @@ constexpr int kTcDense = 0;     // rows [0, M) of A, C in the type of A
 constexpr int kTcLora = 1;      // the same, each tile with the low-rank units of its row block (lora.cu)
 constexpr int kTcGrouped = 2;   // runs of rows with a weight of their own each (experts): offsets on the device
 
+// Whether the CTAs of a cut tile share the sum of its rows at the end, or the one that opened it adds the
+// others' sums in its epilogue. Measured (us, shared against not): 256-row tiles, 295 x 4224 x 1920 with
+// adapters 44 / 71, 844 x 768 x 896 38 / 72; 16-row tiles, 64 experts of 2048 x 1408 44.9 / 40.1.
+__host__ __device__ constexpr bool tc_share(int bn, int mode) { return mode != kTcDense && bn >= 64; }
+
 constexpr int kTcThreads = 768;
 constexpr int kTcWarpLoadW = 0, kTcWarpLoadA = 1, kTcWarpMma = 2, kTcWarpEpi = 4, kTcWarpDeq = 8;
 constexpr int kTcDeqWarps = 16;
@@ -115,7 +122,8 @@ struct TcParams {
     const uint8_t* tiled;
     void* C;
     int* counters;      // one int per tile, zero between calls
-    float* partials;    // [P][BN][128]: sums a CTA publishes for the tile that opens its range
+    float* partials;    // [P][BN][128]: sums a CTA publishes for the tile that opens its range; kTcLora,
+                        // kTcGrouped: [P][2][BN][128], for the cut tiles that open and that end its range
     int* dev_status;
     const int32_t* offsets;   // kTcGrouped: rows offsets[e] .. offsets[e + 1] - 1 meet weight e < E
     int E;
@@ -244,9 +252,10 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int UT = p.K / 128;                              // unit steps per tile
     constexpr bool kGrp = MODE == kTcGrouped, kLora = MODE == kTcLora;
-    const int2* run_tab = reinterpret_cast<const int2*>(smem + p.off_grp);   // kTcGrouped
+    constexpr bool kShare = tc_share(BN, MODE);  // cut tiles are summed at the end, by all their CTAs
+    long long* range = reinterpret_cast<long long*>(smem + p.off_grp);       // kShare, kTcLora: u0, u1, U, P
+    const int2* run_tab = reinterpret_cast<const int2*>(range + 4);          // kTcGrouped
     const int* blk_tab = reinterpret_cast<const int*>(run_tab + p.E);
-    long long* range = reinterpret_cast<long long*>(smem + p.off_grp);       // kTcLora: u0, u1, U, P
     int* cum_tab = reinterpret_cast<int*>(range + 4);                        // kTcLora
     const int cta = blockIdx.x;
     const uint32_t R = p.record;
@@ -311,7 +320,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const int P = kGrp && U < p.P ? (int)U : p.P;
     const bool busy = !kGrp || cta < P;
     const long long u0 = busy ? tc_unit_begin(cta, U, P) : 0, u1 = busy ? tc_unit_begin(cta + 1, U, P) : 0;
-    if constexpr (kLora)
+    if constexpr (kShare || kLora)
         if (threadIdx.x == 0) {
             range[0] = u0;
             range[1] = u1;
@@ -551,6 +560,8 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         // the counter of a cut tile: one per tile (dense), or one per CTA, of the one cut tile that
         // opens in the CTA's range
         auto counter = [&](long long tau, int cf) { return p.counters + (MODE == kTcDense ? tau : (long long)cf); };
+        // where this CTA publishes its sums of a cut tile that CTA cf opened
+        auto own_slot = [&](int cf) { return kShare ? 2 * cta + (cta == cf ? 1 : 0) : cta; };
         // 16 rows from m of the warp's 32 channels, rounded. A lane holds one channel of every row; two
         // exchanges (with lanes 1 and 2 away) give it four channels of every fourth row, so the rows go
         // out in 8-byte stores of 64 bytes per row: a store of 2 bytes per lane and row kept the
@@ -637,7 +648,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     abj[j] ^= 1;
                     if constexpr (kLora) lw.step(1);
                 }
-                if (cf == cl || cta == cf) {
+                if (cf == cl || (!kShare && cta == cf)) {
                     if (cf != cl) {
                         if (leader) {
                             const uint64_t t0 = globaltimer_ns();
@@ -663,7 +674,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 #pragma unroll
                             for (int jj = 0; jj < 16; ++jj) y[jj] = run[c * 16 + jj];
 #pragma unroll 1
-                            for (int cc = cf + 1; cc <= cl; ++cc) {
+                            for (int cc = cf + 1; cc <= cl; ++cc) {   // (!kShare)
                                 const float* part = p.partials + ((size_t)cc * BN + c * 16) * 128 + n;
                                 float pv[16];
 #pragma unroll
@@ -677,7 +688,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     }
                 } else {
                     if (__all_sync(0xffffffffu, ok && !*abort_flag)) {
-                        float* part = p.partials + (size_t)cta * BN * 128;
+                        float* part = p.partials + (size_t)own_slot(cf) * BN * 128;
 #pragma unroll
                         for (int r = 0; r < BN; ++r)
                             if (m0 + r < mend) __stcg(part + (size_t)r * 128 + n, run[r]);
@@ -745,7 +756,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     f(c, y);
                 }
             };
-            if (cf == cl || cta == cf) {
+            if (cf == cl || (!kShare && cta == cf)) {
                 if (cf != cl) {
                     // the tile is cut between CTAs cf .. cl and this is cf: wait until every later
                     // CTA of the tile has published its sums (the tile opens their ranges)
@@ -784,10 +795,10 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     release();
                 }
             } else {
-                // a later CTA of a cut tile (the tile opens its range): publish the sums and count
-                // them, without waiting
+                // a later CTA of a cut tile (the tile opens its range), or (kShare) any CTA of it: publish the
+                // sums and count them, without waiting
                 if (__all_sync(0xffffffffu, ok && !*abort_flag)) {
-                    float* part = p.partials + (size_t)cta * BN * 128;
+                    float* part = p.partials + (size_t)own_slot(cf) * BN * 128;
                     sums([&](int c, float (&y)[16]) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) {
@@ -987,36 +998,111 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 
     tc_fence_before();
     cta_sync();
-    if constexpr (kLora) {
-        // Values of Lb that are not finite entered the products as 0, or they would have reached the other
-        // rows of the block (0 times them); the rows of their adapter get NaN here. Seldom run, and kept
-        // out of the epilogue's loop, where its mere presence cost 5 us per tile. (The flag is seen:
-        // it was set before the unit's weights were handed over, here or by the CTAs of a cut tile.)
-        if (*static_cast<volatile int*>(p.lora_bad) != 0) {
-            // (from shared memory: kept in registers since the start they spilled the roles' loops)
-            const volatile long long* rg = range;
-            const long long U_ = rg[2], u1_ = rg[1];
-            const int P_ = (int)rg[3];
-            TcLoraWalk lw;
-            lw.init(cum_tab, p.K / 128, p.mblocks, rg[0]);
-            for (long long i = rg[0]; i < u1_;) {
-                const long long t1u = i - lw.ku + lw.len;
-                const int m0 = lw.mb * BN, rows = p.M - m0 < BN ? p.M - m0 : BN;
-                if (tc_unit_owner(i - lw.ku, U_, P_) == (int)blockIdx.x)
-                    for (int o = threadIdx.x; o < rows * 128; o += kTcThreads) {
-                        const int m = m0 + (o >> 7), a = p.row_adapter[m];
-                        const size_t ch = (size_t)lw.nt * 128 + (o & 127);
-                        if ((unsigned)a >= (unsigned)p.adapters) continue;
-                        const T* b = static_cast<const T*>(p.lora_b) + ((size_t)a * p.N + ch) * p.rank;
-                        bool bad = false;
-                        for (int j = 0; j < p.rank; ++j) bad = bad || !isfinite(Act<T>::to_f32(b[j]));
-                        if (bad) static_cast<T*>(p.C)[(size_t)m * p.N + ch] = Act<T>::from_f32(__int_as_float(0x7FC00000));
-                    }
-                const long long to = u1_ < t1u ? u1_ : t1u;
-                lw.step((int)(to - i));
-                i = to;
+    if constexpr (kShare || kLora) {
+        // The cut tiles (kShare). All CTAs cf .. cl of a tile have published their sums (or do so soon: none waits
+        // before it has); each adds up, in CTA order, every (cl - cf + 1)-th row of it with all its threads
+        // and writes those rows of C. The counter counts the publishing CTAs, then the finished ones; the
+        // last resets it. (With one CTA's four epilogue warps adding the others' sums, a 256-row tile cut
+        // between six CTAs took 32 us: one L2 round trip per 16 rows and CTA.)
+        // kTcLora: values of Lb that are not finite entered the products as 0, or they would have reached
+        // the other rows of the block (0 times them); the rows of their adapter get NaN here. Kept out of the
+        // epilogue's loop, where its mere presence cost 5 us per tile. (The flag is seen: it was set before
+        // the unit's weights were handed over, here or by the CTAs of a cut tile.)
+        // (The range comes from shared memory: kept in registers since the start it spilled the roles.)
+        const volatile long long* rg = range;
+        const long long b0 = rg[0], b1 = rg[1], U_ = rg[2];
+        const int P_ = (int)rg[3], me = blockIdx.x, UT_ = p.K / 128;
+        auto not_finite = [&](int m, size_t ch) {   // some value of Lb[row m's adapter][ch]
+            const int a = p.row_adapter[m];
+            if ((unsigned)a >= (unsigned)p.adapters) return false;
+            const T* b = static_cast<const T*>(p.lora_b) + ((size_t)a * p.N + ch) * p.rank;
+            bool bad = false;
+            for (int j = 0; j < p.rank; ++j) bad = bad || !isfinite(Act<T>::to_f32(b[j]));
+            return bad;
+        };
+        for (int which = 0; kShare && which < 2 && b0 < b1; ++which) {   // the range's first tile, its last
+            const long long u = which == 0 ? b0 : b1 - 1;
+            long long t0u, t1u;
+            int nt, m0, mend;
+            if constexpr (kLora) {
+                TcLoraWalk w;
+                w.init(cum_tab, UT_, p.mblocks, u);
+                t0u = u - w.ku;
+                t1u = t0u + w.len;
+                nt = w.nt;
+                m0 = w.mb * BN;
+                mend = p.M;
+            } else {
+                MoeWalk w;
+                w.init(run_tab, blk_tab, p.E, p.N / 128, u / UT_);
+                t0u = u / UT_ * UT_;
+                t1u = t0u + UT_;
+                nt = w.nt;
+                m0 = w.row0(BN);
+                mend = w.row_end();
             }
+            const int cf = tc_unit_owner(t0u, U_, P_), cl = tc_unit_owner(t1u - 1, U_, P_), n = cl - cf + 1;
+            if (n == 1 || (which == 0) == (cf == me)) continue;
+            if (threadIdx.x == 0) {
+                const uint64_t t0 = globaltimer_ns();
+                for (;;) {
+                    int c;
+                    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(c) : "l"(p.counters + cf) : "memory");
+                    if (c >= n) break;
+                    if (*abort_flag || globaltimer_ns() - t0 > wait_ns) {
+                        *abort_flag = 1;
+                        report_status(p.dev_status, W4A16_ETIMEOUT);
+                        break;
+                    }
+                }
+            }
+            cta_sync();
+            if (!*abort_flag) {
+                const int rows = mend - m0 < BN ? mend - m0 : BN, mine = (rows - (me - cf) + n - 1) / n;
+                const bool bad = kLora && *static_cast<volatile int*>(p.lora_bad) != 0;
+                for (int o = threadIdx.x; o < mine * 32; o += kTcThreads) {
+                    const int r = (me - cf) + (o >> 5) * n, c4 = 4 * (o & 31);
+                    const float* part = p.partials + (size_t)r * 128 + c4;
+                    float4 y = __ldcg(reinterpret_cast<const float4*>(part + (size_t)(2 * cf + 1) * BN * 128));
+#pragma unroll 4
+                    for (int cc = cf + 1; cc <= cl; ++cc) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(part + (size_t)(2 * cc) * BN * 128));
+                        y.x += v.x;
+                        y.y += v.y;
+                        y.z += v.z;
+                        y.w += v.w;
+                    }
+                    const size_t ch = (size_t)nt * 128 + c4;
+                    if (bad) {
+                        float* f = &y.x;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (not_finite(m0 + r, ch + e)) f[e] = __int_as_float(0x7FC00000);
+                    }
+                    *reinterpret_cast<uint2*>(static_cast<T*>(p.C) + (size_t)(m0 + r) * p.N + ch) =
+                        make_uint2(tc_pack2<T>(y.x, y.y), tc_pack2<T>(y.z, y.w));
+                }
+            }
+            if (threadIdx.x == 0 && atomicAdd(p.counters + cf, 1) == 2 * n - 1) p.counters[cf] = 0;
         }
+        if constexpr (kLora)
+            if (*static_cast<volatile int*>(p.lora_bad) != 0) {   // the other tiles that this CTA has written
+                TcLoraWalk w;
+                w.init(cum_tab, UT_, p.mblocks, b0);
+                for (long long i = b0; i < b1;) {
+                    const long long t1u = i - w.ku + w.len, to = b1 < t1u ? b1 : t1u;
+                    const int m0 = w.mb * BN, rows = p.M - m0 < BN ? p.M - m0 : BN;
+                    if (w.ku == 0 && (!kShare || to == t1u))
+                        for (int o = threadIdx.x; o < rows * 128; o += kTcThreads) {
+                            const int m = m0 + (o >> 7);
+                            const size_t ch = (size_t)w.nt * 128 + (o & 127);
+                            if (not_finite(m, ch))
+                                static_cast<T*>(p.C)[(size_t)m * p.N + ch] = Act<T>::from_f32(__int_as_float(0x7FC00000));
+                        }
+                    w.step((int)(to - i));
+                    i = to;
+                }
+            }
     }
     if (warp == kTcWarpLoadA) {
         tc_fence_after();

@@ -325,7 +325,7 @@ LoraTcPlan plan_lora_tc(int M, int K, int rank, int adapters, int per) {
     pl.rows = (size_t)M < rows ? M : (int)rows;
     pl.mblocks = (pl.rows + pl.bn - 1) / pl.bn;
     pl.S = shrink_slices(pl.rows, K, 32, lora_sm_count());
-    pl.off_part = up256(kGemvStreamCounterBytes + (size_t)lora_sm_count() * pl.bn * 128 * sizeof(float));
+    pl.off_part = up256(kGemvStreamCounterBytes + (size_t)2 * lora_sm_count() * pl.bn * 128 * sizeof(float));
     // S M of any piece: one slice of up to `rows` rows, or at most two CTAs per SM of 32 rows each
     size_t sm = (size_t)64 * lora_sm_count();
     if (sm > (size_t)32 * pl.rows) sm = (size_t)32 * pl.rows;
