@@ -34,12 +34,14 @@ __global__ void __launch_bounds__(kSortThreads) route_hist_kernel(const int32_t*
     pdl_wait();
     pdl_trigger();
     const int lo = blockIdx.x * kRouteHistIds;
+    int e[kRouteHistIds / kSortThreads];
 #pragma unroll
     for (int q = 0; q < kRouteHistIds / kSortThreads; ++q) {
         const int i = lo + q * kSortThreads + threadIdx.x;
-        const int e = i < n ? bin_of(ids[i], E) : -1;
-        count_bin(bins, e, e >= 0);
+        e[q] = i < n ? bin_of(ids[i], E) : -1;
     }
+#pragma unroll
+    for (int q = 0; q < kRouteHistIds / kSortThreads; ++q) count_bin(bins, e[q], e[q] >= 0);
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += kSortThreads) hist[(size_t)blockIdx.x * E + e] = bins[e];
 }
@@ -79,15 +81,22 @@ __global__ void __launch_bounds__(kSortThreads) route_sort_kernel(const RouteSor
             upper[e] = b;
         }
         __syncthreads();
-        for (int i0 = own * kRouteHistIds; i0 < lo; i0 += kSortThreads) {
-            const int i = i0 + tid;
-            const int e = i < lo ? bin_of(p.ids[i], E) : -1;
-            const unsigned active = __ballot_sync(0xffffffffu, e >= 0);
-            if (e >= 0) {
-                const unsigned peers = __match_any_sync(active, e);
-                if (lane == __ffs(peers) - 1) {
-                    atomicAdd(&lower[e], __popc(peers));
-                    atomicSub(&upper[e], __popc(peers));
+        for (int i0 = own * kRouteHistIds; i0 < lo; i0 += 8 * kSortThreads) {   // (once)
+            int e[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const int i = i0 + q * kSortThreads + tid;
+                e[q] = i < lo ? bin_of(p.ids[i], E) : -1;
+            }
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const unsigned active = __ballot_sync(0xffffffffu, e[q] >= 0);
+                if (e[q] >= 0) {
+                    const unsigned peers = __match_any_sync(active, e[q]);
+                    if (lane == __ffs(peers) - 1) {
+                        atomicAdd(&lower[e[q]], __popc(peers));
+                        atomicSub(&upper[e[q]], __popc(peers));
+                    }
                 }
             }
         }
