@@ -370,8 +370,8 @@ W4A16_API int w4a16_gemm_noalloc(const void* A, int a_dtype, int M, int K, const
  *               without a row (a padded or dropped one),
  *   rows[s]   = the flat index i whose sorted row is s,
  *   offsets[e] = first sorted row of expert e, offsets[E] = rows in all (<= T k).
- * One token may name one expert twice: those are two rows. Sorted rows at or past offsets[E] are
- * neither read nor written by any of these entry points: buffers keep what they held there.
+ * One token may name one expert twice: those are two rows. Of sorted rows at or past offsets[E] no
+ * value enters a result, and none of these entry points writes there: buffers keep what they held.
  * Shapes: T >= 1, 1 <= k <= 32, 1 <= E <= 1024, T k <= 2^30, H >= 8, H % 8 == 0.
  *
  * w4a16_moe_sort -- the sort and the gather of the rows, Xs[slots[t, j]] = X[t] (copied bits).
