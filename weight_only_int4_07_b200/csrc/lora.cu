@@ -38,6 +38,7 @@ struct LoraParams {
     float* part;                // [S][M][r]
     int* units;                 // tensor cores: the row blocks' low-rank units and pieces (null: none wanted)
     int* pieces;
+    int* place;                 // [M] a row's adapter's place among those of its row block (-1: none)
     int* bad;
     int bn, max_units, per;
     void* C;
@@ -101,7 +102,7 @@ __device__ __forceinline__ int lora_slots(const LoraParams& p, int m0, int bn, i
     return total;
 }
 
-// The low-rank units and pieces of row block mb, and the flag of values that are not finite.
+// The low-rank units, pieces and places of row block mb, and the flag of values that are not finite.
 __device__ __forceinline__ void lora_list(const LoraParams& p, int mb) {
     __shared__ int slot[kRouteMaxBins];
     __shared__ int wsum[kLoraWarps];
@@ -116,6 +117,10 @@ __device__ __forceinline__ void lora_list(const LoraParams& p, int mb) {
             ++before;
         }
     for (int j = total * pr + threadIdx.x; j < lu * p.per; j += kLoraThreads) pieces[j] = -1;
+    for (int m = mb * p.bn + threadIdx.x; m < min((mb + 1) * p.bn, p.M); m += kLoraThreads) {
+        const int a = p.row_adapter[m];
+        p.place[m] = (unsigned)a < (unsigned)p.L ? slot[a] : -1;
+    }
     if (threadIdx.x == 0) {
         p.units[mb] = lu;
         if (mb == 0) *p.bad = 0;
@@ -220,46 +225,41 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const Lora
 // T as the tensor-core layer takes it. A row block (bn rows) has its adapters in order, each with
 // pr = ceil(r / 16) pieces of 16 ranks, `per` pieces (4 in a bf16 layer, 2 in an fp16 one) to a low-rank
 // unit of 128 columns: per piece [hi | lo] (bf16), or [hi | lo | hi | 0] (fp16, whose Lb is split into hi and
-// lo too). A warp writes one row, all units of its block.
+// lo too). `warps` (1, 2, 4 or 8) warps write one row, all units of its block.
 template <typename T>
-__global__ void __launch_bounds__(kLoraThreads) lora_place_kernel(const LoraParams p, __nv_bfloat16* __restrict__ placed) {
+__global__ void __launch_bounds__(kLoraThreads) lora_place_kernel(const LoraParams p, __nv_bfloat16* __restrict__ placed,
+                                                                  int warps) {
     constexpr int kPer = std::is_same<T, __nv_bfloat16>::value ? 4 : 2;
-    __shared__ int slot[kRouteMaxBins];
-    __shared__ int wsum[kLoraWarps];
     __shared__ __align__(16) __nv_bfloat16 hi[kLoraWarps][kLoraMaxRank], lo[kLoraWarps][kLoraMaxRank];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int row = blockIdx.x * kLoraWarps + warp, m0 = blockIdx.x * kLoraWarps / p.bn * p.bn;
+    const int warp = threadIdx.x >> 5, local = warp / warps, at = threadIdx.x - local * warps * 32, step = 32 * warps;
+    const int row = blockIdx.x * (kLoraWarps / warps) + local;
     const int pr = (p.r + 15) / 16;
     pdl_wait();
     pdl_trigger();
-    int f[4], before;
-    const int lu = (lora_slots(p, m0, p.bn, slot, wsum, f, before) * pr + kPer - 1) / kPer;
-    if (row >= p.M) return;
-    int a = p.row_adapter[row];
-    if ((unsigned)a >= (unsigned)p.L) a = -1;
-    const int mine = a >= 0 ? slot[a] : -1;
-    if (a >= 0) {
-        const float sc = __ldg(p.scale + a);
-        for (int j = lane; j < 16 * pr; j += 32) {
+    const int mine = row < p.M ? __ldcg(p.place + row) : -1;
+    const int columns = row < p.M ? 16 * __ldcg(p.units + row / p.bn) : 0;   // of 8 values
+    if (mine >= 0) {
+        const float sc = __ldg(p.scale + p.row_adapter[row]);
+        for (int j = at; j < 16 * pr; j += step) {
             float s = 0.0f;
             if (j < p.r)
-#pragma unroll 8
+#pragma unroll 16
                 for (int k = 0; k < p.S; ++k) s += __ldcg(p.part + ((size_t)k * p.M + row) * p.r + j);
             s *= sc;
             const __nv_bfloat16 h = __float2bfloat16_rn(s);
-            hi[warp][j] = h;
-            lo[warp][j] = __float2bfloat16_rn(s - __bfloat162float(h));
+            hi[local][j] = h;
+            lo[local][j] = __float2bfloat16_rn(s - __bfloat162float(h));
         }
     }
-    __syncwarp();
+    __syncthreads();
     uint4* out = reinterpret_cast<uint4*>(placed + (size_t)row * p.max_units * 128);
-    for (int q = lane; q < lu * 16; q += 32) {   // 8 columns: unit q / 16, block (q / 4) % 4, part q % 4
+    for (int q = at; q < columns; q += step) {   // unit q / 16, block (q / 4) % 4, part q % 4
         const int b = (q >> 2) & 3, part = q & 3;
-        const int piece = (q >> 4) * kPer + (kPer == 4 ? b : b >> 1);
+        const int piece = (q >> 4) * kPer + (kPer == 4 ? b : b >> 1) - mine * pr;   // of the row's adapter
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (mine >= 0 && piece / pr == mine && !(kPer == 2 && (b & 1) && part >= 2)) {
-            const __nv_bfloat16* src = part < 2 ? hi[warp] : lo[warp];
-            v = *reinterpret_cast<const uint4*>(src + 16 * (piece - mine * pr) + 8 * (part & 1));
+        if (mine >= 0 && (unsigned)piece < (unsigned)pr && !(kPer == 2 && (b & 1) && part >= 2)) {
+            const __nv_bfloat16* src = part < 2 ? hi[local] : lo[local];
+            v = *reinterpret_cast<const uint4*>(src + 16 * piece + 8 * (part & 1));
         }
         out[q] = v;
     }
@@ -310,7 +310,7 @@ struct LoraTcPlan {
     int rows;        // rows of A taken at a time
     int bn, mblocks; // of a piece of `rows` rows
     int S, per, max_units;
-    size_t off_part, off_placed, off_units, off_pieces, off_bad, total;
+    size_t off_part, off_placed, off_units, off_pieces, off_place, off_bad, total;
 };
 
 LoraTcPlan plan_lora_tc(int M, int K, int rank, int adapters, int per) {
@@ -333,7 +333,8 @@ LoraTcPlan plan_lora_tc(int M, int K, int rank, int adapters, int per) {
     pl.off_placed = pl.off_part + up256(sm * rank * 4);
     pl.off_units = pl.off_placed + up256((size_t)pl.rows * pl.max_units * 256);
     pl.off_pieces = pl.off_units + up256((size_t)pl.mblocks * 4);
-    pl.off_bad = pl.off_pieces + up256((size_t)pl.mblocks * pl.max_units * per * 4);
+    pl.off_place = pl.off_pieces + up256((size_t)pl.mblocks * pl.max_units * per * 4);
+    pl.off_bad = pl.off_place + up256((size_t)pl.rows * 4);
     pl.total = pl.off_bad + 256;
     return pl;
 }
@@ -377,13 +378,16 @@ int launch_lora_tc(LoraParams p, const LoraTcPlan& pl, uint8_t* ws, const void* 
     __nv_bfloat16* placed = reinterpret_cast<__nv_bfloat16*>(ws + pl.off_placed);
     p.units = reinterpret_cast<int*>(ws + pl.off_units);
     p.pieces = reinterpret_cast<int*>(ws + pl.off_pieces);
+    p.place = reinterpret_cast<int*>(ws + pl.off_place);
     p.bad = reinterpret_cast<int*>(ws + pl.off_bad);
     p.bn = pl.bn;
     p.max_units = pl.max_units;
     p.per = pl.per;
     if (launch_shrink<4, T>(p, shrink_shares(p.M, p.S, 32, n_sm), stream) != cudaSuccess) return W4A16_ECUDA;
-    if (launch_pdl(lora_place_kernel<T>, dim3((p.M + kLoraWarps - 1) / kLoraWarps), dim3(kLoraThreads), 0, stream, p,
-                   placed) != cudaSuccess)
+    int warps = 1;   // of one row: up to four CTAs per SM in all
+    while (warps < kLoraWarps && (long long)p.M * warps * 2 <= (long long)4 * n_sm * kLoraWarps) warps *= 2;
+    if (launch_pdl(lora_place_kernel<T>, dim3((p.M * warps + kLoraWarps - 1) / kLoraWarps), dim3(kLoraThreads), 0, stream, p,
+                   placed, warps) != cudaSuccess)
         return W4A16_ECUDA;
     CUtensorMap map, map_t;
     if (!make_act_map(&map, p.A, p.M, p.K, pl.bn, dtype == W4A16_BF16) ||
