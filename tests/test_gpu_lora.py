@@ -119,6 +119,24 @@ def test_pieces_of_a_long_batch():
         check(C, A, La, Lb, scale, rows, packed, N, group, sym)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_stretches_of_rows_without_adapters(dtype):
+    """Blocks of rows with many adapters, one or none, in one batch; the slices of K that the rank
+    products are summed in go by how many there are, on the device."""
+    M, K, N, group, sym, r, L = 230, 2048, 256, 128, 0, 40, 40
+    packed, tiled = layer(K, N, group, sym)
+    A, La, Lb, scale, rows = make(M, K, N, r, L, dtype, "any")
+    ws = torch.zeros(native.w4a16_lora_workspace_bytes(M, N, K, group, r, L), dtype=torch.uint8, device="cuda")
+    args = (A.cuda(), tiled, N, group, sym, La.cuda(), Lb.cuda(), scale.cuda())
+    for gaps in ([(0, 32), (64, 128), (200, 230)], [(0, 225)], [(1, 230)], [(0, 0)]):
+        ids = rows.clone()
+        ids[128:160] = 7
+        for lo, hi in gaps:
+            ids[lo:hi] = -1
+        C = native.w4a16_lora_gemm(*args, ids.cuda(), workspace=ws)
+        check(C, A, La, Lb, scale, ids, packed, N, group, sym)
+
+
 @pytest.mark.parametrize("M", [1, 6, 13, 40, 300])
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 def test_an_adapter_that_is_not_finite_stays_with_its_rows(M, dtype):

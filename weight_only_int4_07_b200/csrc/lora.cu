@@ -40,7 +40,8 @@ struct LoraParams {
     int* pieces;
     int* place;                 // [M] a row's adapter's place among those of its row block (-1: none)
     int* bad;
-    int bn, max_units, per;
+    int* slices;                // the slices that the shrink kernel took, of at most S (null: S)
+    int bn, max_units, per, lists;
     void* C;
     int M, K, N, r, L, S;
 };
@@ -127,45 +128,105 @@ __device__ __forceinline__ void lora_list(const LoraParams& p, int mb) {
     }
 }
 
-// T's partial sums over one slice of K (blockIdx.x) for a block of 8 NB rows (blockIdx.y); the adapters
-// of the block are dealt out to gridDim.z CTAs. Warp w takes every eighth 32-K step of the slice; MMA
-// rows are ranks, MMA columns the adapter's rows. With p.units, one more CTA per row block of bn rows
-// (blockIdx.z = gridDim.z - 1) lists its units.
-// RB: 16-rank blocks of one pass over K.
+// T's partial sums. An item is one adapter's rows within a block of 8 NB rows, 16 RB ranks of it and one
+// slice of K; the items are dealt out to the CTAs. How many slices there are goes by the number of
+// items (p.slices: at most p.S, and the kernel says how many it took): 154 rows of 49 adapters have ten
+// times the items of 154 rows of one. Warp w takes every eighth 32-K step of the slice; MMA rows are ranks,
+// MMA columns the adapter's rows. With p.units, the first p.lists CTAs list the row blocks' units instead.
+// RB: 16-rank blocks of one item.
 template <int NB, int RB, typename T>
 __global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const LoraParams p) {
     __shared__ float red[4][RB * NB * 128];
     __shared__ int list[32];
+    __shared__ int before[NB == 1 ? 1 : kLoraMaxChunk / 32 + 1];   // adapters of the blocks before each
     using Ops = GsOps<T>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     pdl_wait();
     pdl_trigger();
-    int shares = gridDim.z;
-    if (p.units && blockIdx.z == --shares) {
-        if (blockIdx.x == 0 && blockIdx.y * 8 * NB % p.bn == 0) lora_list(p, blockIdx.y * 8 * NB / p.bn);
-        // (bn below a block's rows: one row block)
+    if ((int)blockIdx.x < p.lists) {
+        lora_list(p, blockIdx.x);
         return;
     }
-    const LoraBlock blk(p, blockIdx.y * 8 * NB, 8 * NB);
-    const int here = __popc(blk.firsts);
-    for (int nth = blockIdx.z; nth < here; nth += shares) {
+    const int cta = blockIdx.x - p.lists, ctas = gridDim.x - p.lists;
+    const int blocks = (p.M + 8 * NB - 1) / (8 * NB), chunks = (p.r + 16 * RB - 1) / (16 * RB);
+    int S = p.S, pairs;
+    if constexpr (NB == 1) {   // (one block)
+        pairs = __popc(LoraBlock(p, 0, 8).firsts);
+    } else {
+        for (int b0 = warp; b0 < blocks; b0 += 4 * kLoraWarps) {
+            int a[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int m = 32 * (b0 + q * kLoraWarps) + lane;
+                a[q] = m < p.M ? p.row_adapter[m] : -1;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if ((unsigned)a[q] >= (unsigned)p.L) a[q] = -1;
+                const unsigned peers = __match_any_sync(0xffffffffu, a[q]);
+                const int n = __popc(__ballot_sync(0xffffffffu, a[q] >= 0 && __ffs(peers) - 1 == lane));
+                if (lane == 0 && b0 + q * kLoraWarps < blocks) before[b0 + q * kLoraWarps] = n;
+            }
+        }
+        __syncthreads();
+        if (warp == 0) {
+            int base = 0;
+            for (int b = lane; b - lane < blocks; b += 32) {
+                const int n = b < blocks ? before[b] : 0;
+                int x = n;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, x, d);
+                    if (lane >= d) x += y;
+                }
+                if (b < blocks) before[b] = base + x - n;
+                base += __shfl_sync(0xffffffffu, x, 31);
+            }
+            if (lane == 0) before[blocks] = base;
+        }
+        __syncthreads();
+        pairs = before[blocks];
+        if (p.slices) {
+            // the fewest rounds: a CTA's items one after another, each a step per 256 K of its slice and
+            // about four steps' time besides (lane s: s + 1 slices; the fewest slices among equals)
+            const int rounds = (pairs * chunks * (lane + 1) + ctas - 1) / ctas;
+            const int cost = rounds * (4 + (p.K + 256 * (lane + 1) - 1) / (256 * (lane + 1)));
+            const unsigned best = __reduce_min_sync(0xffffffffu, lane < p.S ? (unsigned)cost : 0xffffffffu);
+            S = __ffs(__ballot_sync(0xffffffffu, lane < p.S && (unsigned)cost == best));
+            if (cta == 0 && threadIdx.x == 0) *p.slices = S;
+        }
+    }
+    const int items = pairs * chunks * S;
+    for (int item = cta; item < items; item += ctas) {
+    const int sl = item % S, pc = item / S, r0 = pc % chunks * 16 * RB;
+    int nth = pc / chunks, block = 0;
+    if constexpr (NB > 1) {
+        int hi = blocks - 1;   // the last block with no more than nth adapters before it
+        while (block < hi) {
+            const int m = (block + hi + 1) >> 1;
+            if (before[m] <= nth) block = m;
+            else hi = m - 1;
+        }
+        nth -= before[block];
+    }
+    const LoraBlock blk(p, block * 8 * NB, 8 * NB);
     unsigned left = blk.firsts;
     for (int q = 0; q < nth; ++q) left &= left - 1;
     const int first = __ffs(left) - 1;
     const int adapter = __shfl_sync(0xffffffffu, blk.adapter, first);
     const unsigned same = __shfl_sync(0xffffffffu, blk.peers, first);
     const int n = __popc(same);
-    __syncthreads();   // (the last adapter's rows have been used)
-    if (threadIdx.x < 32 && ((same >> lane) & 1u)) list[__popc(same & ((1u << lane) - 1u))] = blockIdx.y * 8 * NB + lane;
+    __syncthreads();   // (the last item's rows have been used)
+    if (threadIdx.x < 32 && ((same >> lane) & 1u)) list[__popc(same & ((1u << lane) - 1u))] = block * 8 * NB + lane;
     __syncthreads();
     const T* A = static_cast<const T*>(p.A);
     const T* La = static_cast<const T*>(p.La) + (size_t)adapter * p.r * p.K;
-    const int steps = p.K / 32, S = p.S, sl = blockIdx.x;
+    const int steps = p.K / 32;
     const int s0 = (int)((long long)steps * sl / S), s1 = (int)((long long)steps * (sl + 1) / S);
     const T* x[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) x[b] = 8 * b + g < n ? A + (size_t)list[8 * b + g] * p.K + 8 * t : nullptr;
-    for (int r0 = 0; r0 < p.r; r0 += 16 * RB) {
+    {
         float acc[RB][NB][4];
 #pragma unroll
         for (int q = 0; q < RB; ++q)
@@ -217,7 +278,6 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const Lora
             const int at = (((j >> 4) * NB + (m >> 3)) * 4 + (m & 1) + ((j >> 2) & 2)) * 32 + (j & 7) * 4 + ((m & 7) >> 1);
             if (r0 + j < p.r) out[(size_t)list[m] * p.r + r0 + j] = (red[0][at] + red[1][at]) + (red[2][at] + red[3][at]);
         }
-        __syncthreads();
     }
     }
 }
@@ -240,11 +300,12 @@ __global__ void __launch_bounds__(kLoraThreads) lora_place_kernel(const LoraPara
     const int columns = row < p.M ? 16 * __ldcg(p.units + row / p.bn) : 0;   // of 8 values
     if (mine >= 0) {
         const float sc = __ldg(p.scale + p.row_adapter[row]);
+        const int S = __ldcg(p.slices);
         for (int j = at; j < 16 * pr; j += step) {
             float s = 0.0f;
             if (j < p.r)
 #pragma unroll 16
-                for (int k = 0; k < p.S; ++k) s += __ldcg(p.part + ((size_t)k * p.M + row) * p.r + j);
+                for (int k = 0; k < S; ++k) s += __ldcg(p.part + ((size_t)k * p.M + row) * p.r + j);
             s *= sc;
             const __nv_bfloat16 h = __float2bfloat16_rn(s);
             hi[local][j] = h;
@@ -266,19 +327,12 @@ __global__ void __launch_bounds__(kLoraThreads) lora_place_kernel(const LoraPara
 }
 
 // ------------------------------------------------------------------------------ host side
-// K slices of the shrink kernel: about two CTAs per SM when rows share adapters, a 32-K step per warp.
+// K slices of the shrink kernel at most: about two CTAs per SM when rows share adapters, a 32-K step per warp.
 int shrink_slices(int M, int K, int rows, int n_sm) {
     int S = 2 * n_sm / ((M + rows - 1) / rows);
     if (S > 32) S = 32;
     if (S > K / 256) S = K / 256;
     return S < 1 ? 1 : S;
-}
-
-// CTAs that share a row block's adapters: what is left of two per SM. (Eight at all sizes left 2048 rows of
-// four adapters with 1800 CTAs that had nothing to do: 60 us of the launch.)
-int shrink_shares(int M, int S, int rows, int n_sm) {
-    const int n = 2 * n_sm / (S * ((M + rows - 1) / rows));
-    return n < 1 ? 1 : n > rows ? rows : n;
 }
 
 int lora_sm_count() {
@@ -339,12 +393,13 @@ LoraTcPlan plan_lora_tc(int M, int K, int rank, int adapters, int per) {
     return pl;
 }
 
+// ctas: for the items, beside the lists.
 template <int NB, typename T>
-cudaError_t launch_shrink(const LoraParams& p, int shares, cudaStream_t stream) {
-    const dim3 grid(p.S, (p.M + 8 * NB - 1) / (8 * NB), shares + (p.units ? 1 : 0)), block(kLoraThreads);
+cudaError_t launch_shrink(const LoraParams& p, int ctas, cudaStream_t stream) {
+    const dim3 grid(ctas + p.lists), block(kLoraThreads);
     if (p.r <= 16) return launch_pdl(lora_shrink_kernel<NB, 1, T>, grid, block, 0, stream, p);
-    if (p.r <= 32) return launch_pdl(lora_shrink_kernel<NB, 2, T>, grid, block, 0, stream, p);
-    return launch_pdl(lora_shrink_kernel<NB, 4, T>, grid, block, 0, stream, p);
+    if (NB > 1 || p.r <= 32) return launch_pdl(lora_shrink_kernel<NB, 2, T>, grid, block, 0, stream, p);
+    return launch_pdl(lora_shrink_kernel<NB, NB == 1 ? 4 : 2, T>, grid, block, 0, stream, p);
 }
 
 template <typename T>
@@ -352,7 +407,8 @@ int launch_lora_gemv(LoraParams p, const LoraGemvPlan& pl, uint8_t* ws, const vo
                      int* dev_status, cudaStream_t stream) {
     p.S = pl.S;
     p.part = reinterpret_cast<float*>(ws + pl.off_part);
-    if (launch_shrink<1, T>(p, p.M, stream) != cudaSuccess) return W4A16_ECUDA;
+    const int chunks = p.r <= 32 ? 1 : (p.r + 63) / 64;
+    if (launch_shrink<1, T>(p, p.S * p.M * chunks, stream) != cudaSuccess) return W4A16_ECUDA;
     GemvLora lora = {};
     lora.b = p.Lb;
     lora.scale = p.scale;
@@ -380,10 +436,12 @@ int launch_lora_tc(LoraParams p, const LoraTcPlan& pl, uint8_t* ws, const void* 
     p.pieces = reinterpret_cast<int*>(ws + pl.off_pieces);
     p.place = reinterpret_cast<int*>(ws + pl.off_place);
     p.bad = reinterpret_cast<int*>(ws + pl.off_bad);
+    p.slices = p.bad + 1;
+    p.lists = mblocks;
     p.bn = pl.bn;
     p.max_units = pl.max_units;
     p.per = pl.per;
-    if (launch_shrink<4, T>(p, shrink_shares(p.M, p.S, 32, n_sm), stream) != cudaSuccess) return W4A16_ECUDA;
+    if (launch_shrink<4, T>(p, 2 * n_sm, stream) != cudaSuccess) return W4A16_ECUDA;
     int warps = 1;   // of one row: up to four CTAs per SM in all
     while (warps < kLoraWarps && (long long)p.M * warps * 2 <= (long long)4 * n_sm * kLoraWarps) warps *= 2;
     if (launch_pdl(lora_place_kernel<T>, dim3((p.M * warps + kLoraWarps - 1) / kLoraWarps), dim3(kLoraThreads), 0, stream, p,
