@@ -90,6 +90,14 @@ constexpr int kTcGrouped = 2;   // runs of rows with a weight of their own each 
 // adapters 44 / 71, 844 x 768 x 896 38 / 72; 16-row tiles, 64 experts of 2048 x 1408 44.9 / 40.1.
 __host__ __device__ constexpr bool tc_share(int bn, int mode) { return mode != kTcDense && bn >= 64; }
 
+// Units that the exchange of a cut tile's sums costs, beside half a unit for every CTA of the tile: where the
+// CTAs of a tile have no other, and where a range may end one cut tile and open the next. They decide how
+// launches with adapters or experts are cut. Measured (us, cut evenly whatever the sizes against so): 144 rows of 4
+// experts of 768 x 1280 16.0 / 9.9, 3000 of 16 of 1024 x 512 27.3 / 14.9, 11264 of 3 of 6144 x 384 74 / 51; 500 of
+// 4 of 5120 x 640, whose tiles are cut either way, 22.7 / 19.0.
+constexpr int kTcCutOne = 4;
+__host__ __device__ constexpr int tc_cut_two(bool share) { return share ? 14 : 10; }
+
 constexpr int kTcThreads = 768;
 constexpr int kTcWarpLoadW = 0, kTcWarpLoadA = 1, kTcWarpMma = 2, kTcWarpEpi = 4, kTcWarpDeq = 8;
 constexpr int kTcDeqWarps = 16;
@@ -253,7 +261,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const int UT = p.K / 128;                              // unit steps per tile
     constexpr bool kGrp = MODE == kTcGrouped, kLora = MODE == kTcLora;
     constexpr bool kShare = tc_share(BN, MODE);  // cut tiles are summed at the end, by all their CTAs
-    long long* range = reinterpret_cast<long long*>(smem + p.off_grp);       // kShare, kTcLora: u0, u1, U, P
+    long long* range = reinterpret_cast<long long*>(smem + p.off_grp);       // kShare, kTcLora: u0, u1, U, P and pieces
     const int2* run_tab = reinterpret_cast<const int2*>(range + 4);          // kTcGrouped
     const int* blk_tab = reinterpret_cast<const int*>(run_tab + p.E);
     int* cum_tab = reinterpret_cast<int*>(range + 4);                        // kTcLora
@@ -317,15 +325,55 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const long long tiles = (long long)(p.N / 128) * (kGrp ? blk_tab[p.E] : p.mblocks);
     const long long U = tiles * UT + (kLora ? (long long)(p.N / 128) * cum_tab[p.mblocks] : 0);
     // no more ranges than units (the dense launch's host saw to it): none of a tile's ranges is empty
-    const int P = kGrp && U < p.P ? (int)U : p.P;
-    const bool busy = !kGrp || cta < P;
-    const long long u0 = busy ? tc_unit_begin(cta, U, P) : 0, u1 = busy ? tc_unit_begin(cta + 1, U, P) : 0;
+    int P = kGrp && U < p.P ? (int)U : p.P;
+    // How the units are cut (launches of tiles of one length; not the dense ones): ranges of whole tiles
+    // (pieces = 1), each tile into `pieces` ranges of its own, or evenly (0).
+    long long u0 = 0, u1 = 0;
+    int pieces = 0;
+    if constexpr (MODE != kTcDense) {
+        const int len = kLora ? UT + cum_tab[p.mblocks] : UT;
+        if (U > 0 && (kGrp || p.mblocks == 1)) {
+            const long long each = (tiles + P - 1) / P;
+            const long long least = (U + P - 1) / P;
+            const int most = tiles < P ? min((int)(P / tiles), 255) : 1;
+            const long long even = least + tc_cut_two(kShare) + most / 2;
+            int cost = 0x7fffffff;   // in units; lane i: the best of i + 2, i + 34, .. pieces
+            if (each * len > least + kTcCutOne + 1) {
+                for (int n = lane + 2; n <= most && n <= len; n += 32)
+                    cost = min(cost, ((len + n - 1) / n + kTcCutOne + n / 2) * 256 + n);
+                cost = __reduce_min_sync(0xffffffffu, cost);
+            }
+            if (each * len <= min(even, (long long)(cost >> 8))) {
+                pieces = 1;
+                P = (int)((tiles + each - 1) / each);
+                if (cta < P) {
+                    u0 = tc_unit_begin(cta, tiles, P) * len;
+                    u1 = tc_unit_begin(cta + 1, tiles, P) * len;
+                }
+            } else if ((cost >> 8) <= even) {
+                pieces = cost & 255;
+                P = (int)tiles * pieces;
+                if (cta < P) {
+                    const int tile = cta / pieces, q = cta - tile * pieces;
+                    u0 = (long long)tile * len + q * len / pieces;
+                    u1 = (long long)tile * len + (q + 1) * len / pieces;
+                }
+            }
+        }
+    }
+    if (pieces == 0 && cta < P) {
+        u0 = tc_unit_begin(cta, U, P);
+        u1 = tc_unit_begin(cta + 1, U, P);
+    }
+    // the CTAs of a tile [t0u, t1u) that this one has units of
+    auto first_of = [&](long long t0u) { return pieces ? cta - cta % pieces : tc_unit_owner(t0u, U, P); };
+    auto last_of = [&](long long t1u) { return pieces ? cta - cta % pieces + pieces - 1 : tc_unit_owner(t1u - 1, U, P); };
     if constexpr (kShare || kLora)
         if (threadIdx.x == 0) {
             range[0] = u0;
             range[1] = u1;
             range[2] = U;
-            range[3] = P;
+            range[3] = ((long long)pieces << 32) + P;
         }
     const uint32_t tmem_w = tmem + (uint32_t)(kBufs * kIss * kCols);   // the step ring's weight tiles
 
@@ -618,7 +666,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 const int mb = kGrp ? 0 : kLora ? lw.mb : (int)(tau % p.mblocks);
                 const size_t n0 = (size_t)nt * 128;
                 const int m0 = kGrp ? gw.row0(BN) : mb * BN, mend = kGrp ? gw.row_end() : p.M;
-                const int cf = tc_unit_owner(t0u, U, P), cl = tc_unit_owner(t1u - 1, U, P);
+                const int cf = first_of(t0u), cl = last_of(t1u);
                 if (kLora && seg_end > t0u + UT) ahead(nt, mb, lw.len - UT);
                 for (; i < seg_end; ++i) {
                     const int j = kIss == 1 ? 0 : (int)((i - u0) & 1);
@@ -719,7 +767,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             const int mb = kGrp ? 0 : kLora ? lw.mb : (int)(tau % p.mblocks);
             const size_t n0 = (size_t)nt * 128;
             const int m0 = kGrp ? gw.row0(BN) : mb * BN, mend = kGrp ? gw.row_end() : p.M;
-            const int cf = tc_unit_owner(t0u, U, P), cl = tc_unit_owner(t1u - 1, U, P);
+            const int cf = first_of(t0u), cl = last_of(t1u);
             if constexpr (kLora) lw.step((int)(seg_end - i));
             i = seg_end;
             const uint32_t lane_base = tmem + (uint32_t)(ab * kIss * kCols) + ((uint32_t)(32 * q) << 16);
@@ -1011,7 +1059,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         // (The range comes from shared memory: kept in registers since the start it spilled the roles.)
         const volatile long long* rg = range;
         const long long b0 = rg[0], b1 = rg[1], U_ = rg[2];
-        const int P_ = (int)rg[3], me = blockIdx.x, UT_ = p.K / 128;
+        const int P_ = (int)rg[3], pieces_ = (int)(rg[3] >> 32), me = blockIdx.x, UT_ = p.K / 128;
         auto not_finite = [&](int m, size_t ch) {   // some value of Lb[row m's adapter][ch]
             const int a = p.row_adapter[m];
             if ((unsigned)a >= (unsigned)p.adapters) return false;
@@ -1020,7 +1068,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             for (int j = 0; j < p.rank; ++j) bad = bad || !isfinite(Act<T>::to_f32(b[j]));
             return bad;
         };
-        for (int which = 0; kShare && which < 2 && b0 < b1; ++which) {   // the range's first tile, its last
+        for (int which = 0; kShare && which < 2 && b0 < b1 && pieces_ != 1; ++which) {   // the range's first tile, its last
             const long long u = which == 0 ? b0 : b1 - 1;
             long long t0u, t1u;
             int nt, m0, mend;
@@ -1041,7 +1089,8 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 m0 = w.row0(BN);
                 mend = w.row_end();
             }
-            const int cf = tc_unit_owner(t0u, U_, P_), cl = tc_unit_owner(t1u - 1, U_, P_), n = cl - cf + 1;
+            const int cf = pieces_ ? me - me % pieces_ : tc_unit_owner(t0u, U_, P_);
+            const int cl = pieces_ ? cf + pieces_ - 1 : tc_unit_owner(t1u - 1, U_, P_), n = cl - cf + 1;
             if (n == 1 || (which == 0) == (cf == me)) continue;
             if (threadIdx.x == 0) {
                 const uint64_t t0 = globaltimer_ns();
