@@ -30,12 +30,18 @@ int moe_block_rows(int R, int E) {
 // bounds the mean rows of an expert that it accepts.
 bool moe_gemv_rows(int R, int E) { return R <= 8 || (long long)R <= 8ll * E; }
 
-// Few rows per expert: the decode kernel. Measured on 64 experts of 2048 x 1408, decode against
-// tensor cores, by mean rows per expert: group 128 (bf16) 21.3 / 24.7 us at 0.5, 34.9 / 39.5 at 2, 45.4 /
-// 45.0 at 4; group 32 (fp16), where every weight takes a scale multiply in both, 20.3 / 22.2 at 0.5, 26.3 /
-// 26.9 at 1, 34.1 / 33.7 at 2; 8 experts of 4096 x 4096, group 128: 13.3 / 16.1 at one token of two.
-bool moe_few_rows(int R, int E, int group) {
-    return R <= 8 || (long long)R <= (group == 128 ? 3ll * E : (long long)E);
+// Few rows per expert: the decode kernel. Measured, us, decode against tensor cores, by the mean rows of an expert.
+// Experts whose weights keep every SM busy: 64 of 2048 x 1408, group 128 (bf16) 21.3 / 25.9 at 0.5, 39.6 / 46.6 at 2,
+// 45.3 / 49.6 at 4, 50.5 / 51.0 at 6; group 32 (fp16), where every weight takes a scale multiply in both, 21.0 / 22.5
+// at 0.5, 42.6 / 42.9 at 3, 44.6 / 44.2 at 4; 8 of 4096 x 4096 34.0 / 38.4 at 4 (group 128), 32.6 / 35.9 at 3 (32).
+// Below 32 unit records per SM (all experts') the tensor cores' whole tiles end sooner: 16 of 1024 x 768 9.2 / 9.9 at
+// 0.5, 11.7 / 10.0 at 1, 13.3 / 10.1 at 2; 64 of 1024 x 384 11.4 / 10.3 at 0.5, 13.3 / 10.4 at 1; 8 of 2048 x 2048
+// 13.0 / 14.3 at 1, 15.9 / 14.3 at 2; 8 of 1024 x 1024 10.0 / 9.7 at 1; 4 of 768 x 1280 9.0 / 8.5 at 1, 10.3 / 8.5 at 2.
+bool moe_few_rows(int R, int E, int N, int K, int group) {
+    int n_sm = gemv_stream_sm_count();
+    if (n_sm <= 0) n_sm = 148;
+    if ((long long)E * (N / 128) * (K / 128) < 32ll * n_sm) return R <= (E < 8 ? E : 8) || R <= E / 2;
+    return R <= 8 || (long long)R <= (group == 128 ? 4ll * E : 3ll * E);
 }
 
 TcPlan plan_moe_tc(int R, int E, int N, int K, int group, int sym) {
@@ -55,7 +61,7 @@ size_t moe_gemm_partial_bytes(int R, int E, int K) {
 
 int launch_moe_gemm(const void* A, int a_dtype, int R, int K, const void* tiled, int E, const int32_t* offsets, int N,
                     int group, int sym, void* C, void* workspace, int kernel, int* dev_status, cudaStream_t stream) {
-    if (kernel == W4A16_KERNEL_GEMV || (kernel == W4A16_KERNEL_AUTO && moe_few_rows(R, E, group))) {
+    if (kernel == W4A16_KERNEL_GEMV || (kernel == W4A16_KERNEL_AUTO && moe_few_rows(R, E, N, K, group))) {
         if (!moe_gemv_rows(R, E)) return W4A16_EUNSUPPORTED;
         const int st = launch_moe_gemv(A, a_dtype, R, K, tiled, E, offsets, N, group, sym, C, workspace, dev_status, stream);
         if (st != W4A16_EUNSUPPORTED || kernel == W4A16_KERNEL_GEMV) return st;
