@@ -24,6 +24,8 @@
 // counter. The result does not depend on timing.
 // (Launches with adapters or experts, from 64 rows per tile: every CTA of a cut tile publishes, and
 // all of them add up a share of its rows once their ranges are done; tc_share.)
+// (They also choose, from the number and length of their tiles, between this cut, ranges of whole tiles, and ranges
+// that each lie within one tile; kTcCutOne.)
 //
 // Warp roles (768 threads):
 //   warp 0      : weight loader -- one bulk copy per two unit records (codes, scales and zeros

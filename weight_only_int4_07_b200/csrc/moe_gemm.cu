@@ -14,9 +14,9 @@ namespace {
 // Rows per tile from the mean rows of an expert (the host knows no more). A tile's cost goes mostly by its
 // weights (dequantized once per tile) and little by its rows, so it should hold most experts' rows at
 // once. Measured, us at tiles of 16 / 32 / 64 / 128 / 256 rows, 16 experts of 4096 x 4096 (bf16, group 128;
-// even routing): mean 6: 68 / 69 / 75 / 87 / 94, 16: 97 / 71 / 77 / 88 / 95, 40: 186 / 128 / 79 / 90 / 97, 100:
-// 399 / 233 / 140 / 96 / 105, 256: 966 / 523 / 294 / 209 / 179; uneven routing moves the best up: mean 10: 74 / 65 /
-// 71, 24: 126 / 91 / 82 / 89, 160: 613 / 337 / 205 / 158 / 146.
+// even routing): mean 6: 69 / 71 / 81 / 92 / 96, 16: 96 / 72 / 82 / 92 / 97, 40: 186 / 129 / 84 / 94 / 100, 100:
+// 399 / 232 / 141 / 102 / 108, 256: 961 / 518 / 303 / 215 / 181; uneven routing moves the best up: mean 10: 75 / 66 /
+// 74, 24: 127 / 93 / 85 / 94, 160: 613 / 335 / 212 / 165 / 151.
 int moe_block_rows(int R, int E) {
     const int mean = (R + E - 1) / E;
     if (mean <= 4) return 16;
