@@ -119,6 +119,18 @@ def test_pieces_of_a_long_batch():
         check(C, A, La, Lb, scale, rows, packed, N, group, sym)
 
 
+# one row block: its tiles whole (one or several to a CTA), each in ranges of its own, or cut evenly
+CUTS = [(100, 512, 2304, 32, 1, torch.bfloat16, 16, 3, "any"), (40, 256, 20480, 128, 0, torch.float16, 8, 2, "any"),
+        (200, 4096, 384, 128, 0, torch.bfloat16, 64, 8, "any"), (30, 4096, 256, 64, 1, torch.float16, 32, 9, "any"),
+        (12, 4096, 640, 128, 0, torch.bfloat16, 24, 6, "any"), (70, 5120, 10240, 128, 0, torch.bfloat16, 16, 4, "any"),
+        (20, 5120, 10240, 64, 0, torch.float16, 16, 4, "any")]
+
+
+@pytest.mark.parametrize("M,K,N,group,sym,dtype,r,L,ids", CUTS)
+def test_tiles_whole_in_ranges_of_their_own_or_cut_evenly(M, K, N, group, sym, dtype, r, L, ids):
+    test_rows_with_their_adapters(M, K, N, group, sym, dtype, r, L, ids)
+
+
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 def test_stretches_of_rows_without_adapters(dtype):
     """Blocks of rows with many adapters, one or none, in one batch; the slices of K that the rank

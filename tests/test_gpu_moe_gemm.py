@@ -114,6 +114,18 @@ def test_every_run_meets_its_own_weight(counts, K, N, group, sym, dtype, kernel)
     check(C, A, off, packed, K, N, group, sym)
 
 
+# the tensor cores' tiles whole (one or several to a CTA), each in ranges of its own, or cut evenly
+CUTS = [([30, 40, 0, 35], 768, 1280, 32, 1, torch.bfloat16), ([30] * 20, 256, 2304, 128, 0, torch.float16),
+        ([60, 70], 4096, 384, 128, 0, torch.bfloat16), ([300, 1], 2048, 256, 64, 1, torch.float16),
+        ([10, 14], 4096, 384, 64, 0, torch.float16), ([2, 3, 0, 4], 2560, 256, 128, 0, torch.bfloat16),
+        ([45] * 10, 5120, 1024, 128, 0, torch.bfloat16), ([12] * 10, 5120, 1024, 128, 0, torch.float16)]
+
+
+@pytest.mark.parametrize("counts,K,N,group,sym,dtype", CUTS)
+def test_tiles_whole_in_ranges_of_their_own_or_cut_evenly(counts, K, N, group, sym, dtype):
+    test_every_run_meets_its_own_weight(counts, K, N, group, sym, dtype, native.KERNEL_TC)
+
+
 @pytest.mark.parametrize("kernel", KERNELS)
 def test_offsets_outside_the_rows_are_clamped(kernel):
     K, N, group, sym = 256, 256, 128, 0

@@ -352,7 +352,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     u0 = tc_unit_begin(cta, tiles, P) * len;
                     u1 = tc_unit_begin(cta + 1, tiles, P) * len;
                 }
-            } else if ((cost >> 8) <= even) {
+            } else if (cost != 0x7fffffff && (cost >> 8) <= even) {
                 pieces = cost & 255;
                 P = (int)tiles * pieces;
                 if (cta < P) {
