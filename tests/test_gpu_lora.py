@@ -231,3 +231,21 @@ def test_captured_and_replayed_on_other_rows(M):
         torch.cuda.synchronize()
         assert torch.equal(C, D)
         check(C, *new, packed, N, group, sym)
+
+
+@pytest.mark.parametrize("M", [1, 5])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_a_part_of_the_input_that_is_zero_or_tiny(M, dtype):
+    """A CTA of the decode kernel stages a part of K: rows that are zero (or, bf16, tiny) there while their
+    rank products are not, and a product far above the layer's (bf16: 2^34; fp16: 2^10)."""
+    K, N, group, sym, r, L = 1024, 128, 128, 0, 16, 2
+    packed, tiled = layer(K, N, group, sym)
+    for lo, hi, by in ((0, 128, 0.0), (0, 512, 0.0), (512, 1024, 0.0), (0, 512, 2.0 ** -90), (0, 1024, 0.0)):
+        if dtype == torch.float16 and by:
+            continue
+        for up in (1.0, 2.0 ** 16 if dtype == torch.bfloat16 else 2.0 ** 4):
+            A, La, Lb, scale, rows = make(M, K, N, r, L, dtype, "one")
+            A[:, lo:hi] *= by
+            La, Lb = La * up, Lb * up
+            C = native.w4a16_lora_gemm(A.cuda(), tiled, N, group, sym, La.cuda(), Lb.cuda(), scale.cuda(), rows.cuda())
+            check(C, A, La, Lb, scale, rows, packed, N, group, sym)

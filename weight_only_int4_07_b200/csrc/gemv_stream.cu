@@ -233,6 +233,8 @@ __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(c
     const T* A = static_cast<const T*>(p.A) + (size_t)sl * K;
 
     bool wide = false;   // kConv: some row keeps bf16 values and the bf16 arithmetic
+    auto row_shift = [&](int m) { return min(max(rowexp[m] - 141, -100), 114); };   // row m's k
+    auto row_up = [&](int m) { return __int_as_float((127 + row_shift(m)) << 23); };
 
     // The units of K this CTA's range touches: all of them when the range holds a whole tile, else
     // a run of nneed units from sp0, wrapping at the end of the tile. Only their activations are
@@ -362,8 +364,7 @@ __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(c
         cta_sync();
         for (int m = 0; m < M; ++m) wide = wide || rowexp[m] - rowmin[m] > 31;
         for (int m = 0; m < M && !wide; ++m) {
-            const int k = min(max(rowexp[m] - 141, -100), 114);
-            const float down = __int_as_float((127 - k) << 23);
+            const float down = __int_as_float((127 - row_shift(m)) << 23);
             for (int c0 = threadIdx.x; c0 < nchunk; c0 += kGsThreads) {
                 int sp;
                 const int c = chunk_of(c0, sp);
@@ -382,8 +383,7 @@ __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(c
         }
     }
     if constexpr (LO) {
-        // t in the scale of this CTA's sums (kConv: times its rows' 2^-k), as hi + lo; ranks past the
-        // last are zeros
+        // t as hi + lo; ranks past the last are zeros
         for (int i = threadIdx.x; i < M * (lts - p.lora.rank); i += kGsThreads) {
             const int m = i / (lts - p.lora.rank), j = p.lora.rank + i - m * (lts - p.lora.rank);
             lt[m * lts + j] = lt[(M + m) * lts + j] = __float2bfloat16_rn(0.0f);
@@ -393,12 +393,9 @@ __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(c
             const int i = threadIdx.x + h * kGsThreads;
             if (i < M * p.lora.rank) {
                 const int m = i / p.lora.rank, j = i - m * p.lora.rank;
-                float x = tv[h];
-                if constexpr (kConv)
-                    if (!wide) x *= __int_as_float((127 - min(max(rowexp[m] - 141, -100), 114)) << 23);
-                const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+                const __nv_bfloat16 hi = __float2bfloat16_rn(tv[h]);
                 lt[m * lts + j] = hi;
-                lt[(M + m) * lts + j] = __float2bfloat16_rn(x - __bfloat162float(hi));
+                lt[(M + m) * lts + j] = __float2bfloat16_rn(tv[h] - __bfloat162float(hi));
             }
         }
     }
@@ -599,9 +596,19 @@ __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(c
         }
     };
 
-    // LO, compute warps: the pieces of this group added to tot, for channels ch0 + 8 r of the tile
+    // LO, compute warps: the pieces of this group added to tot, for channels ch0 + 8 r of the tile. kConv:
+    // tot is first taken back to the scale of A. (t in the scale of tot left FP32 where the part of A that
+    // this CTA stages is far smaller than the whole row: by 2^114 where it is zero.)
     auto low_rank = [&](int tile) {
         using B = GsOps<__nv_bfloat16>;
+        if constexpr (kConv)
+            if (!wide) {
+                const float up0 = row_up(2 * t), up1 = row_up(2 * t + 1);
+#pragma unroll
+                for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) tot[rt][0][e] *= e & 1 ? up1 : up0;
+            }
         const unsigned peers = __match_any_sync(0xffffffffu, mine);
         unsigned left = __ballot_sync(0xffffffffu, mine >= 0 && __ffs(peers) - 1 == lane);
         // the adapters of this lane's result columns, rows 2 t and 2 t + 1: a piece's sums count for the rows
@@ -732,8 +739,8 @@ __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(c
             if (cf == cl || cta == cf) {
                 for (int m = 0; m < M; ++m) {
                     float up = 1.0f;
-                    if constexpr (kConv)   // undo the row's 2^-k
-                        if (!wide) up = __int_as_float((127 + min(max(rowexp[m] - 141, -100), 114)) << 23);
+                    if constexpr (kConv)   // undo the row's 2^-k (low_rank has done so, in the first slice)
+                        if (!wide && !(LO && sl == 0)) up = row_up(m);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int ch = lane + 32 * j;
@@ -755,7 +762,7 @@ __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(c
                 for (int m = 0; m < M; ++m) {
                     float up = 1.0f;
                     if constexpr (kConv)   // undo the row's 2^-k (this CTA's)
-                        if (!wide) up = __int_as_float((127 + min(max(rowexp[m] - 141, -100), 114)) << 23);
+                        if (!wide) up = row_up(m);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int ch = lane + 32 * j;
