@@ -170,6 +170,27 @@ def test_wide_bf16_rows(kernel):
     check(C, A, off, packed, K, N, group, sym)
 
 
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("e", [-110, -118, -122, -128])
+def test_bf16_rows_at_the_low_end(kernel, e):
+    """bf16 rows near and below the type's smallest normal value, 2^-126: as exact as any others (below
+    it the output's own steps of 2^-133 count)."""
+    K, N, group, sym = 1024, 256, 128, 0
+    packed, tiled = experts(2, K, N, group, sym)
+    off = offsets_of([4, 3])
+    A = (activations(7, K, torch.float64, 8) * 2.0 ** e).bfloat16()
+    A[1] = 0
+    A[5, 128:] *= 2.0 ** 12
+    C = native.w4a16_moe_gemm(A.cuda(), off.cuda(), tiled, N, group, sym, kernel=kernel)
+    if e > -128:
+        check(C, A, off, packed, K, N, group, sym)
+    for x, (c, s, z) in enumerate(packed):
+        rows = slice(int(off[x]), int(off[x + 1]))
+        Y, mag = oracle.linear(bits(A[rows]), 1, c, s, z, N, group, sym)
+        err = np.abs(C[rows].cpu().double().numpy() - Y)
+        assert (err <= (2.0 ** -8 + K * 2.0 ** -23) * mag + 2.0 ** -8 * np.abs(Y) + TINY[torch.bfloat16]).all()
+
+
 def test_routing_experts_and_back_in_a_captured_graph():
     """A mixture layer as it is used: sort, two expert products with a gate between, back; captured
     once and replayed on other tokens, against the oracle and the same calls made eagerly."""

@@ -648,3 +648,20 @@ def test_naive_path_within_bound(M, a_dtype):
         torch.backends.cuda.matmul.allow_fp16_reduced_precision_reduction = prev
         torch.backends.cuda.matmul.allow_bf16_reduced_precision_reduction = prev_bf
     _check_gemm(C, Ab, a_dtype, oc, os_, oz, N, group, sym)
+
+
+@pytest.mark.parametrize("e", [-110, -118, -122])
+@pytest.mark.parametrize("M", [1, 3, 8, 16])
+def test_bf16_rows_at_the_low_end(M, e):
+    """bf16 rows near the type's smallest normal value, 2^-126, at group 128: within the bound of any other
+    rows, relative to their terms (h = 2^-8: the weight's and the output's rounding)."""
+    K, N, group, sym = 1024, 256, 128, 0
+    _, (oc, os_, oz), (gc, gs, gz) = _quantized("normal", K, N, group, sym, 3)
+    tiled = native.w4a16_repack(gc, gs, gz, K, N, group, sym)
+    A = (torch.randn(M, K, generator=torch.Generator().manual_seed(M), dtype=torch.float64) * 2.0 ** e).bfloat16()
+    A[M // 2, 512:] = 0
+    C = native.w4a16_gemm(A.cuda(), tiled, None, None, N, group, sym, layout=native.LAYOUT_TILED)
+    Y, mag = oracle.linear(_to_np16(A), synthetic.BF16, oc, os_, oz, N, group, sym)
+    err = np.abs(oracle.decode16(_to_np16(C), synthetic.BF16) - Y)
+    assert (err <= (2.0 ** -8 + K * 2.0 ** -23) * mag + 2.0 ** -8 * np.abs(Y) + 2.0 ** -133).all()
+    assert (err ** 2).sum() <= 2.0 ** -16 * (Y ** 2).sum()

@@ -40,6 +40,13 @@ struct GsMasks {
     uint32_t lo, hi, magic, m4, m8, m12;
 };
 
+// bf16 activations that the decode kernels convert to fp16 (group 128): the k of the power of two 2^-k that
+// takes a row whose largest biased exponent is `top` to a largest value in [2^14, 2^15), at least -126: both
+// 2^-k and 2^k are FP32 normals, and with k = -126 every value below 2^-111, subnormals among them, still
+// lands on the fp16 grid (bf16's smallest step 2^-133 becomes 2^-7).
+__device__ __forceinline__ int half_shift(int top) { return min(max(top - 141, -126), 114); }
+__device__ __forceinline__ float pow2_f32(int k) { return __int_as_float((127 + k) << 23); }   // -126 <= k <= 127
+
 template <typename T>
 struct GsOps;
 

@@ -233,8 +233,7 @@ __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(c
     const T* A = static_cast<const T*>(p.A) + (size_t)sl * K;
 
     bool wide = false;   // kConv: some row keeps bf16 values and the bf16 arithmetic
-    auto row_shift = [&](int m) { return min(max(rowexp[m] - 141, -100), 114); };   // row m's k
-    auto row_up = [&](int m) { return __int_as_float((127 + row_shift(m)) << 23); };
+    auto row_up = [&](int m) { return pow2_f32(half_shift(rowexp[m])); };   // row m's 2^k
 
     // The units of K this CTA's range touches: all of them when the range holds a whole tile, else
     // a run of nneed units from sp0, wrapping at the end of the tile. Only their activations are
@@ -364,7 +363,7 @@ __global__ void __launch_bounds__(kGsThreads, kGsCtasPerSm) gemv_stream_kernel(c
         cta_sync();
         for (int m = 0; m < M; ++m) wide = wide || rowexp[m] - rowmin[m] > 31;
         for (int m = 0; m < M && !wide; ++m) {
-            const float down = __int_as_float((127 - row_shift(m)) << 23);
+            const float down = pow2_f32(-half_shift(rowexp[m]));
             for (int c0 = threadIdx.x; c0 < nchunk; c0 += kGsThreads) {
                 int sp;
                 const int c = chunk_of(c0, sp);

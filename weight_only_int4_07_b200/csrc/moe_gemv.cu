@@ -198,9 +198,9 @@ __global__ void __launch_bounds__(kMgActThreads) moe_acts_kernel(const T* __rest
         for (int d = 8; d > 0; d >>= 1) ee = __vmaxu2(ee, __shfl_xor_sync(0xffffffffu, ee, d));
         const int top = (int)(ee >> 16);
         wide = top - (255 - (int)(ee & 0xFFFFu)) > 31;
-        k = min(max(top - 141, -100), 114);   // the largest value to [2^14, 2^15)
+        k = half_shift(top);
         if (!wide) {
-            const float down = __int_as_float((127 - k) << 23);
+            const float down = pow2_f32(-k);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const __half2 y = __floats2half2_rn(__uint_as_float(xw[q] << 16) * down,
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kMgActThreads) moe_acts_kernel(const T* __rest
     if (POST && c == 0) {
         MgNote n;
         n.sum = sum * 5.9604644775390625e-08f;   // 2^-24
-        n.up = __int_as_float((127 + k) << 23);
+        n.up = pow2_f32(k);
         n.wide = wide;
         n.pad = 0;
         *reinterpret_cast<MgNote*>(dst + 64) = n;
