@@ -438,7 +438,8 @@ W4A16_API int w4a16_moe_combine_grad(const void* dY, const void* Ys, int dtype, 
  *   workspace, ws_bytes   device, at least w4a16_moe_workspace_bytes(R, E, N, K, group) bytes, 16-byte
  *              aligned, under the contract of w4a16_gemm's workspace (first 64 KiB zero before the
  *              first call; calls that share one ordered on the GPU; zeroed again after
- *              W4A16_ETIMEOUT). It may be shared with w4a16_gemm.
+ *              W4A16_ETIMEOUT). It may be shared with w4a16_gemm. The size grows with R: one for the most
+ *              rows serves every call with fewer.
  *   kernel     W4A16_KERNEL_AUTO (by the mean rows of an expert, R / E), or a forced
  *              W4A16_KERNEL_GEMV (the decode kernel; R <= max(8, 8 E), else W4A16_EUNSUPPORTED) or
  *              W4A16_KERNEL_TC.
@@ -472,7 +473,8 @@ W4A16_API int w4a16_moe_gemm(const void* A, int a_dtype, int R, int K, const voi
  *   workspace, ws_bytes   device, at least w4a16_lora_workspace_bytes(M, N, K, group, rank, adapters)
  *              bytes, 16-byte aligned, under the contract of w4a16_gemm's workspace. It may be
  *              shared with w4a16_gemm. It holds the rank products of at most 64 MiB or 256 rows at a
- *              time, whichever is more, and of at most 16384 rows; longer batches are taken in pieces.
+ *              time, whichever is more, and of at most 16384 rows; longer batches are taken in pieces. The
+ *              size grows with M: one for the largest batch serves every smaller one.
  *   dev_status device int or NULL: W4A16_ETIMEOUT as for w4a16_gemm.
  *   stream     cudaStream_t. Two or three kernel launches (each piece).
  * Values that are not finite: those of a row of A, of an adapter or of its scale reach only the rows that

@@ -423,3 +423,16 @@ def test_lora_rejects_bad_arguments_before_any_launch(L):
     assert call(ws=None) == native.EWORKSPACE
     assert call(wsb=need - 1) == native.EWORKSPACE
     assert call(ws=mis) == native.EALIGN
+
+
+@pytest.mark.parametrize("N,K,group", [(8192, 1408, 128), (57344, 8192, 128), (128, 28672, 32), (768, 1280, 64)])
+def test_a_workspace_for_many_rows_serves_fewer(L, N, K, group):
+    """The routed layers' workspace sizes never fall as a batch grows."""
+    rows = list(range(1, 80)) + [127, 128, 129, 255, 256, 257, 511, 512, 513, 1023, 1024, 1025, 2048, 2049, 4096, 8192,
+                                 8193, 16384, 16385, 40000, 1 << 20]
+    for E in (1, 3, 8, 128, 1024):
+        need = [native.w4a16_moe_workspace_bytes(R, E, N, K, group) for R in rows]
+        assert need == sorted(need) and need[0] > 0
+    for rank, adapters in ((8, 1), (16, 14), (128, 64), (256, 1024)):
+        need = [native.w4a16_lora_workspace_bytes(M, N, K, group, rank, adapters) for M in rows]
+        assert need == sorted(need) and need[0] > 0

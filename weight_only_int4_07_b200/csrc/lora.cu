@@ -469,11 +469,15 @@ int launch_lora_tc(LoraParams p, const LoraTcPlan& pl, uint8_t* ws, const void* 
 }  // namespace
 
 size_t lora_workspace_bytes(int M, int N, int K, int group, int rank, int adapters) {
-    // the larger need over both types and both forms, so that a forced kernel also fits
+    // the largest need over both types and both forms, so that a forced kernel also fits, and over all batches
+    // of up to M rows (the tensor cores' grows with M)
     const size_t a = plan_lora_tc(M, K, rank, adapters, 2).total, b = plan_lora_tc(M, K, rank, adapters, 4).total;
-    const size_t tc = a > b ? a : b;
-    const size_t gemv = lora_gemv_fits(M, rank) ? plan_lora_gemv(M, N, K, group, rank).total : 0;
-    return tc > gemv ? tc : gemv;
+    size_t most = a > b ? a : b;
+    for (int m = 1; m <= M && lora_gemv_fits(m, rank); ++m) {
+        const size_t gemv = plan_lora_gemv(m, N, K, group, rank).total;
+        if (gemv > most) most = gemv;
+    }
+    return most;
 }
 
 int launch_lora_gemm(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,

@@ -28,7 +28,7 @@ int moe_block_rows(int R, int E) {
 
 // The decode kernel takes blocks of 8 rows; it lays the rows' activations out in the workspace, which
 // bounds the mean rows of an expert that it accepts.
-bool moe_gemv_rows(int R, int E) { return R <= 8 || (long long)R <= 8ll * E; }
+int moe_gemv_max_rows(int E) { return 8 * E; }
 
 // Few rows per expert: the decode kernel. Measured, us, decode against tensor cores, by the mean rows of an expert.
 // Experts whose weights keep every SM busy: 64 of 2048 x 1408, group 128 (bf16) 21.3 / 25.9 at 0.5, 39.6 / 46.6 at 2,
@@ -52,17 +52,20 @@ TcPlan plan_moe_tc(int R, int E, int N, int K, int group, int sym) {
 
 }  // namespace
 
+// Room for R rows and for any fewer: the decode kernel's records count up to the most rows that it accepts, also
+// where R itself is beyond them. (Both terms grow with R.)
 size_t moe_gemm_partial_bytes(int R, int E, int K) {
     int n_sm = gemv_stream_sm_count();
     if (n_sm <= 0) n_sm = 148;
-    const size_t tc = (size_t)2 * n_sm * moe_block_rows(R, E) * 128 * sizeof(float), gemv = moe_gemv_rows(R, E) ? moe_gemv_partial_bytes(R, K) : 0;
+    const size_t tc = (size_t)2 * n_sm * moe_block_rows(R, E) * 128 * sizeof(float);
+    const size_t gemv = moe_gemv_partial_bytes(R < moe_gemv_max_rows(E) ? R : moe_gemv_max_rows(E), K);
     return tc > gemv ? tc : gemv;
 }
 
 int launch_moe_gemm(const void* A, int a_dtype, int R, int K, const void* tiled, int E, const int32_t* offsets, int N,
                     int group, int sym, void* C, void* workspace, int kernel, int* dev_status, cudaStream_t stream) {
     if (kernel == W4A16_KERNEL_GEMV || (kernel == W4A16_KERNEL_AUTO && moe_few_rows(R, E, N, K, group))) {
-        if (!moe_gemv_rows(R, E)) return W4A16_EUNSUPPORTED;
+        if (R > moe_gemv_max_rows(E)) return W4A16_EUNSUPPORTED;
         const int st = launch_moe_gemv(A, a_dtype, R, K, tiled, E, offsets, N, group, sym, C, workspace, dev_status, stream);
         if (st != W4A16_EUNSUPPORTED || kernel == W4A16_KERNEL_GEMV) return st;
     }
