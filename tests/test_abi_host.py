@@ -436,3 +436,25 @@ def test_a_workspace_for_many_rows_serves_fewer(L, N, K, group):
     for rank, adapters in ((8, 1), (16, 14), (128, 64), (256, 1024)):
         need = [native.w4a16_lora_workspace_bytes(M, N, K, group, rank, adapters) for M in rows]
         assert need == sorted(need) and need[0] > 0
+
+
+_ROUTED_CALLS = ("import ctypes; from weight_only_int4_07_b200 import native; L = native.lib(); "
+                 "p = ctypes.c_void_p(1 << 20); "
+                 "moe = lambda R, E, kernel=0: L.w4a16_moe_gemm(p, 0, R, 4096, p, E, p, 4096, 128, 0, p, p, 1 << 30, kernel, None, None); "
+                 "lora = lambda M, r: L.w4a16_lora_gemm(p, 0, M, 4096, p, 4096, 128, 0, p, p, p, 3, r, p, p, p, 1 << 30, None, None); "
+                 "moe(8, 8); moe(400, 8); moe(8, 8, 2); lora(4, 16); lora(40, 16); lora(8, 256)")
+
+
+def _kernels_logged(env):
+    r = _in_child(dict(env, W4A16_LOG="1", CUDA_VISIBLE_DEVICES=""), _ROUTED_CALLS)
+    assert r.returncode == 0, r.stderr
+    lines = [x for x in r.stderr.splitlines() if x.startswith("[w4a16]")]
+    assert lines[0].startswith("[w4a16] moe gemm R=8 E=8 N=4096 K=4096 g=128 sym=0 -> ")
+    assert lines[3].startswith("[w4a16] lora gemm M=4 N=4096 K=4096 g=128 sym=0 rank=16 adapters=3 -> ")
+    return [x.rsplit(" -> ")[1] for x in lines]
+
+
+def test_log_environment_prints_the_routed_layers_kernels(L):
+    """W4A16_LOG=1: one line per product of the routed layers, with the kernel it takes (as above, the
+    calls then fail on the host without a device)."""
+    assert _kernels_logged({}) == ["gemv", "tc", "tc", "gemv", "tc", "tc"]

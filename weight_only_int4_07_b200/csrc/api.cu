@@ -400,9 +400,11 @@ W4A16_API int w4a16_moe_gemm(const void* A, int a_dtype, int R, int K, const voi
     if (!aligned16(A) || !aligned16(tiled) || !aligned16(offsets) || !aligned16(C)) return W4A16_EALIGN;
     if (!workspace || ws_bytes < w4a16_moe_workspace_bytes(R, E, N, K, group)) return W4A16_EWORKSPACE;
     if (!aligned16(workspace)) return W4A16_EALIGN;
+    const int chosen = kernel == W4A16_KERNEL_AUTO ? moe_select_kernel(R, E, N, K, group, sym) : kernel;
     if (log_enabled())
-        fprintf(stderr, "[w4a16] moe gemm R=%d E=%d N=%d K=%d g=%d sym=%d\n", R, E, N, K, group, sym);
-    return launch_moe_gemm(A, a_dtype, R, K, tiled, E, offsets, N, group, sym, C, workspace, kernel, dev_status,
+        fprintf(stderr, "[w4a16] moe gemm R=%d E=%d N=%d K=%d g=%d sym=%d -> %s\n", R, E, N, K, group, sym,
+                kernel_name(chosen));
+    return launch_moe_gemm(A, a_dtype, R, K, tiled, E, offsets, N, group, sym, C, workspace, chosen, dev_status,
                            static_cast<cudaStream_t>(stream));
 }
 
@@ -435,8 +437,8 @@ W4A16_API int w4a16_lora_gemm(const void* A, int a_dtype, int M, int K, const vo
     if (!workspace || ws_bytes < lora_workspace_bytes(M, N, K, group, rank, adapters)) return W4A16_EWORKSPACE;
     if (!aligned16(workspace)) return W4A16_EALIGN;
     if (log_enabled())
-        fprintf(stderr, "[w4a16] lora gemm M=%d N=%d K=%d g=%d sym=%d rank=%d adapters=%d\n", M, N, K, group, sym,
-                rank, adapters);
+        fprintf(stderr, "[w4a16] lora gemm M=%d N=%d K=%d g=%d sym=%d rank=%d adapters=%d -> %s\n", M, N, K, group, sym,
+                rank, adapters, kernel_name(lora_select_kernel(M, N, K, group, rank)));
     return launch_lora_gemm(A, a_dtype, M, K, tiled, N, group, sym, lora_a, lora_b, lora_scale, adapters, rank,
                             row_adapter, C, workspace, dev_status, static_cast<cudaStream_t>(stream));
 }

@@ -480,6 +480,13 @@ size_t lora_workspace_bytes(int M, int N, int K, int group, int rank, int adapte
     return most;
 }
 
+int lora_select_kernel(int M, int N, int K, int group, int rank) {
+    return lora_gemv_fits(M, rank) && w4a16_select_kernel(M, N, K, group) == W4A16_KERNEL_GEMV &&
+                   plan_lora_gemv(M, N, K, group, rank).total
+               ? W4A16_KERNEL_GEMV
+               : W4A16_KERNEL_TC;
+}
+
 int launch_lora_gemm(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
                      const void* La, const void* Lb, const float* scale, int adapters, int rank,
                      const int32_t* row_adapter, void* C, void* workspace, int* dev_status, cudaStream_t stream) {
@@ -497,11 +504,10 @@ int launch_lora_gemm(const void* A, int a_dtype, int M, int K, const void* tiled
     p.N = N;
     p.r = rank;
     p.L = adapters;
-    if (lora_gemv_fits(M, rank) && w4a16_select_kernel(M, N, K, group) == W4A16_KERNEL_GEMV) {
+    if (lora_select_kernel(M, N, K, group, rank) == W4A16_KERNEL_GEMV) {
         const LoraGemvPlan pl = plan_lora_gemv(M, N, K, group, rank);
-        if (pl.total)
-            return bf16 ? launch_lora_gemv<__nv_bfloat16>(p, pl, ws, tiled, group, sym, a_dtype, dev_status, stream)
-                        : launch_lora_gemv<__half>(p, pl, ws, tiled, group, sym, a_dtype, dev_status, stream);
+        return bf16 ? launch_lora_gemv<__nv_bfloat16>(p, pl, ws, tiled, group, sym, a_dtype, dev_status, stream)
+                    : launch_lora_gemv<__half>(p, pl, ws, tiled, group, sym, a_dtype, dev_status, stream);
     }
     const LoraTcPlan pl = plan_lora_tc(M, K, rank, adapters, bf16 ? 4 : 2);
     for (int m0 = 0; m0 < M; m0 += pl.rows) {

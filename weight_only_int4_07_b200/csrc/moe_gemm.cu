@@ -62,12 +62,17 @@ size_t moe_gemm_partial_bytes(int R, int E, int K) {
     return tc > gemv ? tc : gemv;
 }
 
+int moe_select_kernel(int R, int E, int N, int K, int group, int sym) {
+    return moe_few_rows(R, E, N, K, group) && R <= moe_gemv_max_rows(E) && moe_gemv_fits(R, E, N, K, group, sym)
+               ? W4A16_KERNEL_GEMV
+               : W4A16_KERNEL_TC;
+}
+
 int launch_moe_gemm(const void* A, int a_dtype, int R, int K, const void* tiled, int E, const int32_t* offsets, int N,
                     int group, int sym, void* C, void* workspace, int kernel, int* dev_status, cudaStream_t stream) {
-    if (kernel == W4A16_KERNEL_GEMV || (kernel == W4A16_KERNEL_AUTO && moe_few_rows(R, E, N, K, group))) {
+    if (kernel == W4A16_KERNEL_GEMV) {
         if (R > moe_gemv_max_rows(E)) return W4A16_EUNSUPPORTED;
-        const int st = launch_moe_gemv(A, a_dtype, R, K, tiled, E, offsets, N, group, sym, C, workspace, dev_status, stream);
-        if (st != W4A16_EUNSUPPORTED || kernel == W4A16_KERNEL_GEMV) return st;
+        return launch_moe_gemv(A, a_dtype, R, K, tiled, E, offsets, N, group, sym, C, workspace, dev_status, stream);
     }
     const TcPlan pl = plan_moe_tc(R, E, N, K, group, sym);
     if (!pl.ok) return W4A16_EUNSUPPORTED;

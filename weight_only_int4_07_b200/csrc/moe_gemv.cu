@@ -510,9 +510,8 @@ struct MgPlan {
     size_t smem;
 };
 
-MgPlan plan_moe_gemv(int R, int E, int N, int K, int group, int sym) {
+MgPlan plan_moe_gemv(int R, int E, int N, int K, int group, int sym, int n_sm) {
     MgPlan pl = {};
-    const int n_sm = gemv_stream_sm_count();
     if (R < 1 || E < 1 || K % 128 != 0 || N % 128 != 0 || K < 128 || N < 128 || n_sm <= 0) return pl;
     const TiledLayout L = tiled_layout(K, N, group, sym);
     pl.rows = R < kMgMaxRows ? R : kMgMaxRows;
@@ -580,11 +579,17 @@ static size_t moe_gemv_sum_bytes(int R) {
     return (size_t)n_sm * (R < kMgMaxRows ? R : kMgMaxRows) * 128 * sizeof(float);
 }
 
+// (without a device to ask, as where it has 148 SMs)
+bool moe_gemv_fits(int R, int E, int N, int K, int group, int sym) {
+    const int n_sm = gemv_stream_sm_count();
+    return plan_moe_gemv(R, E, N, K, group, sym, n_sm > 0 ? n_sm : 148).ok;
+}
+
 size_t moe_gemv_partial_bytes(int R, int K) { return moe_gemv_sum_bytes(R) + (size_t)R * (K / 128) * kMgRowBytes; }
 
 int launch_moe_gemv(const void* A, int a_dtype, int R, int K, const void* tiled, int E, const int32_t* offsets, int N,
                     int group, int sym, void* C, void* workspace, int* dev_status, cudaStream_t stream) {
-    const MgPlan pl = plan_moe_gemv(R, E, N, K, group, sym);
+    const MgPlan pl = plan_moe_gemv(R, E, N, K, group, sym, gemv_stream_sm_count());
     if (!pl.ok) return W4A16_EUNSUPPORTED;
     const TiledLayout L = tiled_layout(K, N, group, sym);
     const bool bf16 = a_dtype == W4A16_BF16;

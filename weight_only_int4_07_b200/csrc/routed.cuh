@@ -42,6 +42,8 @@ size_t moe_gemm_partial_bytes(int R, int E, int K);
 size_t moe_gemv_partial_bytes(int R, int K);
 int launch_moe_gemv(const void* A, int a_dtype, int R, int K, const void* tiled, int E, const int32_t* offsets, int N,
                     int group, int sym, void* C, void* workspace, int* dev_status, cudaStream_t stream);
+bool moe_gemv_fits(int R, int E, int N, int K, int group, int sym);
+int moe_select_kernel(int R, int E, int N, int K, int group, int sym);   // what AUTO takes: W4A16_KERNEL_GEMV or _TC
 int launch_moe_gemm(const void* A, int a_dtype, int R, int K, const void* tiled, int E, const int32_t* offsets, int N,
                     int group, int sym, void* C, void* workspace, int kernel, int* dev_status, cudaStream_t stream);
 
@@ -60,6 +62,7 @@ int launch_gemv_lora(const void* A, int a_dtype, int M, int K, const void* tiled
 // The layer with low-rank adapters.
 constexpr int kLoraMaxRank = 256;
 size_t lora_workspace_bytes(int M, int N, int K, int group, int rank, int adapters);
+int lora_select_kernel(int M, int N, int K, int group, int rank);   // W4A16_KERNEL_GEMV or _TC
 int launch_lora_gemm(const void* A, int a_dtype, int M, int K, const void* tiled, int N, int group, int sym,
                      const void* La, const void* Lb, const float* scale, int adapters, int rank,
                      const int32_t* row_adapter, void* C, void* workspace, int* dev_status, cudaStream_t stream);
