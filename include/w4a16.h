@@ -276,7 +276,8 @@ W4A16_API size_t w4a16_workspace_bytes(int M, int N, int K, int group);
  * Small M is bound by the weight stream and goes to the decode GEMV (W4A16_KERNEL_GEMV); larger M
  * goes to the tensor-core GEMM ("INT8 vs INT4 Quantization, in depth", section "Two regimes:
  * waiting for memory, waiting for math"). The plain layout always runs the CUDA-core GEMV.
- * The environment variable W4A16_FORCE_KERNEL=gemv|tc overrides the choice.
+ * The environment variable W4A16_FORCE_KERNEL=gemv|tc overrides the choice (that of w4a16_lora_gemm, which
+ * is this one up to 8 rows, and of w4a16_moe_gemm too, where the kernel named can serve the call).
  * On the tiled layout the decode GEMV is the persistent stream-K kernel (one CTA per SM, unit
  * records streamed by bulk copies, warp-level tensor-core MMA). When the M rows of A for the
  * whole K do not fit in its shared memory it runs over S equal slices of K (each served by its
@@ -440,8 +441,9 @@ W4A16_API int w4a16_moe_combine_grad(const void* dY, const void* Ys, int dtype, 
  *              first call; calls that share one ordered on the GPU; zeroed again after
  *              W4A16_ETIMEOUT). It may be shared with w4a16_gemm. The size grows with R: one for the most
  *              rows serves every call with fewer.
- *   kernel     W4A16_KERNEL_AUTO (by the mean rows of an expert, R / E), or a forced
- *              W4A16_KERNEL_GEMV (the decode kernel; R <= max(8, 8 E), else W4A16_EUNSUPPORTED) or
+ *   kernel     W4A16_KERNEL_AUTO (by the mean rows of an expert, R / E; W4A16_FORCE_KERNEL=gemv|tc
+ *              overrides the choice where the kernel named can serve the call), or a forced
+ *              W4A16_KERNEL_GEMV (the decode kernel; R <= 8 E, else W4A16_EUNSUPPORTED) or
  *              W4A16_KERNEL_TC.
  *   dev_status device int or NULL: W4A16_ETIMEOUT as for w4a16_gemm.
  *   stream     cudaStream_t. Two kernel launches (decode: the activations are laid out first) or one.

@@ -458,3 +458,13 @@ def test_log_environment_prints_the_routed_layers_kernels(L):
     """W4A16_LOG=1: one line per product of the routed layers, with the kernel it takes (as above, the
     calls then fail on the host without a device)."""
     assert _kernels_logged({}) == ["gemv", "tc", "tc", "gemv", "tc", "tc"]
+
+
+def test_force_kernel_environment_reaches_the_routed_layers(L):
+    """W4A16_FORCE_KERNEL overrides AUTO wherever the kernel it names can serve the call; a kernel that the
+    caller names stays."""
+    assert _kernels_logged({"W4A16_FORCE_KERNEL": "tc"}) == ["tc"] * 6
+    assert _kernels_logged({"W4A16_FORCE_KERNEL": "gemv"}) == ["gemv", "tc", "tc", "gemv", "tc", "tc"]   # 400 rows of 8: too many
+    r = _in_child({"W4A16_FORCE_KERNEL": "gemv", "W4A16_LOG": "1", "CUDA_VISIBLE_DEVICES": ""},
+                  _ROUTED_CALLS.replace("moe(400, 8)", "moe(60, 8)"))
+    assert "R=60 E=8 N=4096 K=4096 g=128 sym=0 -> gemv" in r.stderr

@@ -400,7 +400,7 @@ W4A16_API int w4a16_moe_gemm(const void* A, int a_dtype, int R, int K, const voi
     if (!aligned16(A) || !aligned16(tiled) || !aligned16(offsets) || !aligned16(C)) return W4A16_EALIGN;
     if (!workspace || ws_bytes < w4a16_moe_workspace_bytes(R, E, N, K, group)) return W4A16_EWORKSPACE;
     if (!aligned16(workspace)) return W4A16_EALIGN;
-    const int chosen = kernel == W4A16_KERNEL_AUTO ? moe_select_kernel(R, E, N, K, group, sym) : kernel;
+    const int chosen = kernel == W4A16_KERNEL_AUTO ? moe_select_kernel(R, E, N, K, group, sym, forced_kernel()) : kernel;
     if (log_enabled())
         fprintf(stderr, "[w4a16] moe gemm R=%d E=%d N=%d K=%d g=%d sym=%d -> %s\n", R, E, N, K, group, sym,
                 kernel_name(chosen));

@@ -62,8 +62,9 @@ size_t moe_gemm_partial_bytes(int R, int E, int K) {
     return tc > gemv ? tc : gemv;
 }
 
-int moe_select_kernel(int R, int E, int N, int K, int group, int sym) {
-    return moe_few_rows(R, E, N, K, group) && R <= moe_gemv_max_rows(E) && moe_gemv_fits(R, E, N, K, group, sym)
+int moe_select_kernel(int R, int E, int N, int K, int group, int sym, int forced) {
+    const bool want = forced == W4A16_KERNEL_AUTO ? moe_few_rows(R, E, N, K, group) : forced == W4A16_KERNEL_GEMV;
+    return want && R <= moe_gemv_max_rows(E) && moe_gemv_fits(R, E, N, K, group, sym)
                ? W4A16_KERNEL_GEMV
                : W4A16_KERNEL_TC;
 }

@@ -43,7 +43,8 @@ size_t moe_gemv_partial_bytes(int R, int K);
 int launch_moe_gemv(const void* A, int a_dtype, int R, int K, const void* tiled, int E, const int32_t* offsets, int N,
                     int group, int sym, void* C, void* workspace, int* dev_status, cudaStream_t stream);
 bool moe_gemv_fits(int R, int E, int N, int K, int group, int sym);
-int moe_select_kernel(int R, int E, int N, int K, int group, int sym);   // what AUTO takes: W4A16_KERNEL_GEMV or _TC
+// What AUTO takes, W4A16_KERNEL_GEMV or _TC; forced: the environment's choice, if any (where it can serve the call).
+int moe_select_kernel(int R, int E, int N, int K, int group, int sym, int forced);
 int launch_moe_gemm(const void* A, int a_dtype, int R, int K, const void* tiled, int E, const int32_t* offsets, int N,
                     int group, int sym, void* C, void* workspace, int kernel, int* dev_status, cudaStream_t stream);
 
