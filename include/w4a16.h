@@ -447,6 +447,9 @@ W4A16_API int w4a16_moe_combine_grad(const void* dY, const void* Ys, int dtype, 
  *              W4A16_KERNEL_TC.
  *   dev_status device int or NULL: W4A16_ETIMEOUT as for w4a16_gemm.
  *   stream     cudaStream_t. Two kernel launches (decode: the activations are laid out first) or one.
+ * Rounding. C once; the dequantized weight once to the type of A before it is multiplied, except at group 128
+ *   in the decode kernel and in 16-row tiles, which scale the FP32 sums of a group instead (against 64
+ *   bits, 1.35 to 1.4 times the error of the output's rounding alone where weights are rounded).
  * Ordering. The decode kernel reads the offsets and weights while its own first kernel still runs,
  * which in turn lets it start only after everything before the call has completed: no condition
  * on the kernels before the call.
@@ -460,8 +463,13 @@ W4A16_API int w4a16_moe_gemm(const void* A, int a_dtype, int R, int K, const voi
 /*
  * w4a16_lora_gemm -- the layer with low-rank adapters of many requests at once:
  *   C[m] = A[m] . dequant(W) + scale_a (A[m] . La_a^T) . Lb_a^T,  a = row_adapter[m],
- *   the first term alone where row_adapter[m] is outside [0, adapters). All sums in FP32, C rounded
- *   once. Rows that share an adapter share its reads; nothing depends on their order.
+ *   the first term alone where row_adapter[m] is outside [0, adapters). All sums in FP32. Rows that share an
+ *   adapter share its reads; nothing depends on their order.
+ * Rounding. C once. The dequantized weight as in w4a16_gemm: once to the type of A before it is multiplied,
+ *   except where the decode kernel (up to 8 rows) or 16-row tiles (up to 16) scale the FP32 sums of a
+ *   group instead, at group 128; so the last bits of a row depend on how many rows share the call. The
+ *   rank products scale_a A[m] . La_a^T, formed in FP32, enter the second product as two bf16 values, 16
+ *   significant bits of each (fewer below 2^-118, where bf16 has no smaller steps).
  * Arguments
  *   A, a_dtype, M, K, tiled, N, group, sym   as for w4a16_gemm on the TILED layout (K and N multiples of
  *              128, else W4A16_EUNSUPPORTED).

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kLoraThreads, 2) lora_shrink_kernel(const Lora
     using Ops = GsOps<T>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     pdl_wait();
-    pdl_trigger();
+    pdl_trigger();   // (after the wait: the decode layer reads before its own, pdl.cuh)
     if ((int)blockIdx.x < p.lists) {
         lora_list(p, blockIdx.x);
         return;
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kLoraThreads) lora_place_kernel(const LoraPara
     const int row = blockIdx.x * (kLoraWarps / warps) + local;
     const int pr = (p.r + 15) / 16;
     pdl_wait();
-    pdl_trigger();
+    pdl_trigger();   // (after the wait: the layer reads and writes before its own, pdl.cuh)
     const int mine = row < p.M ? __ldcg(p.place + row) : -1;
     const int columns = row < p.M ? 16 * __ldcg(p.units + row / p.bn) : 0;   // of 8 values
     if (mine >= 0) {

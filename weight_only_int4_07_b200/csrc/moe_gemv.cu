@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kMgActThreads) moe_acts_kernel(const T* __rest
                                                                  uint8_t* __restrict__ acts) {
     constexpr bool kConv = POST && std::is_same<T, __nv_bfloat16>::value;
     pdl_wait();
-    pdl_trigger();
+    pdl_trigger();   // (after the wait: moe_gemv_kernel reads and writes before its own, pdl.cuh)
     const int c = threadIdx.x & 15;
     const long long item = (long long)blockIdx.x * (kMgActThreads / 16) + (threadIdx.x >> 4);
     const long long items = (long long)R * (K / 128);

@@ -22,10 +22,20 @@ inline bool allow_smem(F* kernel, size_t bytes, std::atomic<uint64_t>& done) {
     return true;
 }
 
-// All kernels before this one on the stream have completed and their writes are visible. A kernel
-// launched with launch_pdl runs it before it touches any buffer that another kernel may use.
+// The kernel before this one on the stream has completed and its writes are visible. What holds of the
+// kernels launched with launch_pdl:
+//  - Every kernel runs it (some thread of each CTA) before it ends, so that a kernel which has completed has
+//    all kernels before it completed too.
+//  - A kernel runs it before it touches any buffer that another kernel may use, with two exceptions that read
+//    and write early, what their own first kernel leaves aside: moe_gemv_kernel (only its producer waits,
+//    for the activation records of moe_acts_kernel) and tc_gemm_kernel<.., kTcLora> (only its activation
+//    loader waits, for the T of lora_place_kernel).
+//  - The kernel before such an early one (moe_acts_kernel, lora_place_kernel; lora_shrink_kernel before
+//    gemv_stream_kernel, which reads weights and adapters early) triggers only after its own wait: when the
+//    early one starts, everything before that kernel has completed. A trigger moved above the wait there
+//    would be a race.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// The next kernel's CTAs may start as this grid's CTAs leave their SMs.
+// The next kernel may start once every CTA of this grid has run this (or left).
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" :::); }
 
 template <typename... P, typename... A>
