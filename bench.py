@@ -49,7 +49,8 @@ SWEEP_MS = (1, 2, 4, 8, 16, 32, 64, 128, 256, 512, 2048)
 # ncu DRAM traffic of the decode kernel, written by hand from a capture into this file, with the
 # hash of the kernel sources it was taken on (the bench reports it only while they match)
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "gemv_stream_traffic.txt")   # JSON
-DECODE_SOURCES = ("gemv_stream.cu", "sm100_ptx.cuh", "tiled_layout.cuh", "common.cuh")
+DECODE_SOURCES = ("gemv_stream.cu", "common.cuh", "dequant.cuh", "pdl.cuh", "routed.cuh", "sm100_ptx.cuh",
+                  "tiled_layout.cuh")   # the kernel's file and every one that it includes
 
 
 # ----------------------------------------------------------------------------- work model

@@ -71,6 +71,22 @@ def test_decode_traffic_record_applies_only_to_its_sources(tmp_path, monkeypatch
     assert b is None and info["stale"]
 
 
+def test_decode_sources_are_all_that_the_decode_kernel_includes():
+    """The hash behind the traffic record covers gemv_stream.cu and every file of csrc that it includes,
+    directly or through another."""
+    import re
+
+    csrc = os.path.join(bench.ROOT, "weight_only_int4_07_b200", "csrc")
+    seen, todo = set(), ["gemv_stream.cu"]
+    while todo:
+        name = todo.pop()
+        if name in seen or not os.path.exists(os.path.join(csrc, name)):   # (include/w4a16.h: no kernel code)
+            continue
+        seen.add(name)
+        todo += re.findall(r'#include "([^"]+)"', open(os.path.join(csrc, name)).read())
+    assert set(bench.DECODE_SOURCES) == seen
+
+
 def test_algorithmic_bytes_match_the_format():
     """0.515625 byte/weight for g128 with an FP16 scale; + 0.5/128 with INT4 zero-points."""
     K, N = 4096, 4096
