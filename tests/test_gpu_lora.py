@@ -249,3 +249,40 @@ def test_a_part_of_the_input_that_is_zero_or_tiny(M, dtype):
             La, Lb = La * up, Lb * up
             C = native.w4a16_lora_gemm(A.cuda(), tiled, N, group, sym, La.cuda(), Lb.cuda(), scale.cuda(), rows.cuda())
             check(C, A, La, Lb, scale, rows, packed, N, group, sym)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_slices_of_k_where_rows_are_zero(dtype):
+    """8 rows of 8192 inputs, which the decode kernel takes in slices of K: rows that are zero in the first or
+    in the last slices, one row all zero."""
+    M, K, N, group, sym, r, L = 8, 8192, 256, 128, 0, 16, 3
+    packed, tiled = layer(K, N, group, sym)
+    A, La, Lb, scale, rows = make(M, K, N, r, L, dtype, "any")
+    A[:3, :K // 2] = 0
+    A[3:6, K // 2:] = 0
+    A[6] = 0
+    C = native.w4a16_lora_gemm(A.cuda(), tiled, N, group, sym, La.cuda(), Lb.cuda(), scale.cuda(), rows.cuda())
+    check(C, A, La, Lb, scale, rows, packed, N, group, sym)
+
+
+# the down projections' input lengths, of which a CTA of the decode kernel stages a part
+LONG = [(1, 14336, 256, 128, 0, torch.float16, 16, 2, "one"), (1, 28672, 128, 128, 1, torch.bfloat16, 64, 3, "one"),
+        (3, 14336, 128, 64, 0, torch.bfloat16, 32, 3, "any"), (8, 28672, 128, 128, 0, torch.bfloat16, 16, 5, "any"),
+        (8, 14336, 384, 128, 0, torch.float16, 64, 8, "any"), (7, 28672, 256, 32, 0, torch.float16, 8, 4, "wild"),
+        (16, 28672, 128, 128, 0, torch.bfloat16, 32, 9, "any"), (40, 14336, 256, 128, 1, torch.bfloat16, 16, 7, "any"),
+        (40, 28672, 128, 32, 0, torch.float16, 40, 3, "runs")]
+
+
+@pytest.mark.parametrize("M,K,N,group,sym,dtype,r,L,ids", LONG)
+def test_long_inputs(M, K, N, group, sym, dtype, r, L, ids):
+    test_rows_with_their_adapters(M, K, N, group, sym, dtype, r, L, ids)
+
+
+# several hundred rows in no order: every block of 256 meets most adapters
+UNORDERED = [(542, 1152, 384, 128, 0, torch.float16, 112, 36, "any"), (700, 512, 256, 64, 1, torch.bfloat16, 64, 64, "any"),
+             (384, 2048, 256, 128, 0, torch.bfloat16, 128, 40, "wild"), (900, 256, 128, 32, 0, torch.float16, 16, 300, "any")]
+
+
+@pytest.mark.parametrize("M,K,N,group,sym,dtype,r,L,ids", UNORDERED)
+def test_many_rows_in_no_order(M, K, N, group, sym, dtype, r, L, ids):
+    test_rows_with_their_adapters(M, K, N, group, sym, dtype, r, L, ids)

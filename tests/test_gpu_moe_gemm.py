@@ -126,6 +126,49 @@ def test_tiles_whole_in_ranges_of_their_own_or_cut_evenly(counts, K, N, group, s
     test_every_run_meets_its_own_weight(counts, K, N, group, sym, dtype, native.KERNEL_TC)
 
 
+# the down projections' input lengths; an expert with most of the rows beside many with few or none
+LONG = [([1, 0, 3], 14336, 128, 128, 0, torch.bfloat16), ([2, 1], 28672, 128, 128, 1, torch.float16),
+        ([0, 9, 4, 1], 14336, 128, 32, 1, torch.float16), ([12, 30], 28672, 128, 64, 0, torch.bfloat16)]
+UNEVEN = [([1] * 60 + [300] + [2] * 40 + [0] * 20 + [15] * 5 + [1, 0], 256, 128, 128, 0, torch.bfloat16),
+          ([0] * 127 + [384], 256, 128, 32, 0, torch.float16),
+          ([1] * 31 + [90], 384, 256, 64, 1, torch.bfloat16)]
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("counts,K,N,group,sym,dtype", LONG + UNEVEN)
+def test_long_inputs_and_uneven_routing(counts, K, N, group, sym, dtype, kernel):
+    test_every_run_meets_its_own_weight(counts, K, N, group, sym, dtype, kernel)
+
+
+@pytest.mark.parametrize("kernel,most,dtype", [(native.KERNEL_GEMV, 6, torch.float16), (native.KERNEL_GEMV, 6, torch.bfloat16),
+                                               (native.KERNEL_AUTO, 2, torch.bfloat16), (native.KERNEL_TC, 6, torch.float16),
+                                               (native.KERNEL_TC, 30, torch.float16), (native.KERNEL_TC, 80, torch.bfloat16),
+                                               (native.KERNEL_TC, 180, torch.bfloat16), (native.KERNEL_TC, 300, torch.float16)])
+def test_as_many_experts_as_a_call_takes(kernel, most, dtype):
+    """1024 experts (the runs' table takes 12 KB of shared memory) at every tile height; 0 to `most` rows
+    each, the first and the last expert with some. Experts' outputs are checked on a sample of them."""
+    E, K, N, group, sym = 1024, 128, 128, 32, 0
+    packed, tiled = experts(E, K, N, group, sym)
+    counts = torch.randint(0, most + 1, (E,), generator=torch.Generator().manual_seed(most))
+    counts[[0, 517, E - 1]] = most
+    counts[[1, 516, E - 2]] = 0
+    off = offsets_of(counts.tolist())
+    n = int(off[E])
+    A = activations(n + 2, K, dtype, 9)
+    C = torch.full((n + 2, N), 5.0, dtype=dtype, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    native.w4a16_moe_gemm(A.cuda(), off.cuda(), tiled, N, group, sym, C=C, kernel=kernel, dev_status=status)
+    assert int(status) == 0 and bool((C[n:] == 5.0).all())
+    dt, h = (0 if dtype == torch.float16 else 1), torch.finfo(dtype).eps / 2
+    for e in [0, 2, 3, 515, 517, 518, E - 3, E - 1] + list(range(7, E, 61)):
+        rows = slice(int(off[e]), int(off[e + 1]))
+        if rows.start == rows.stop:
+            continue
+        Y, mag = oracle.linear(bits(A[rows]), dt, *packed[e], N, group, sym)
+        err = np.abs(C[rows].cpu().double().numpy() - Y)
+        assert (err <= (h + K * 2.0 ** -23) * mag + h * np.abs(Y) + TINY[dtype]).all(), e
+
+
 @pytest.mark.parametrize("kernel", KERNELS)
 def test_offsets_outside_the_rows_are_clamped(kernel):
     K, N, group, sym = 256, 256, 128, 0
@@ -246,3 +289,44 @@ def test_routing_experts_and_back_in_a_captured_graph():
         ref, mag = routed.combine(ys.cpu().double().numpy(), slots, w.cpu().numpy())
         assert (np.abs(y.cpu().double().numpy() - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -21 * mag).all()
         assert not bool(y[5].any())
+
+
+def test_the_way_back_through_experts_in_16_bits():
+    """A mixture layer's gradients as a program forms them: combine's, each expert's product with its
+    dequantized weight (a library product: the layer's own way back is not this library's), sort's.
+    Against the formulas in 64 bits; h = eps / 2: one rounding each of dYs, of dXs and of dX, and of
+    Ys in dw, beside FP32 sums."""
+    T, k, E, K, N, group, sym = 40, 3, 6, 256, 128, 128, 0
+    packed, tiled = experts(E, K, N, group, sym)
+    g = torch.Generator().manual_seed(4)
+    ids = torch.randint(0, E, (T, k), generator=g, dtype=torch.int32)
+    ids[3], ids[7, 1] = -1, -1
+    X, dY = (torch.randn(T, n, generator=g).half() for n in (K, N))
+    w = torch.rand(T, k, generator=g)
+    offsets, _, slots, Xs = native.w4a16_moe_sort(ids.cuda(), E, X=X.cuda())
+    Ys = native.w4a16_moe_gemm(Xs, offsets, tiled, N, group, sym)
+    dYs, dw = native.w4a16_moe_combine_grad(dY.cuda(), Ys, slots, w.cuda())
+    weights = [oracle.dequant(*packed[e], K, N, group, sym) for e in range(E)]
+    dXs = torch.zeros_like(Xs)
+    off = offsets.tolist()
+    for e in range(E):
+        W = torch.from_numpy(weights[e]).cuda()
+        dXs[off[e]:off[e + 1]] = (dYs[off[e]:off[e + 1]].double() @ W.t()).half()
+    dX = native.w4a16_moe_sort_grad(dXs, slots).cpu().double().numpy()
+    h = 2.0 ** -11
+    Xd, dYd, wd, ys = X.double().numpy(), dY.double().numpy(), w.double().numpy(), Ys.cpu().double().numpy()
+    dw, sl = dw.cpu().double().numpy(), slots.cpu().numpy()
+    for t in range(T):
+        ref, mag = np.zeros(K), np.zeros(K)
+        for j in range(k):
+            e = int(ids[t, j])
+            if e < 0:
+                assert dw[t, j] == 0
+                continue
+            ref += wd[t, j] * (weights[e] @ dYd[t])
+            mag += wd[t, j] * (np.abs(weights[e]) @ np.abs(dYd[t]))
+            y, ymag = Xd[t] @ weights[e], np.abs(Xd[t]) @ np.abs(weights[e])
+            # Ys as the layer leaves it, within its own bound; dw a sum of N products of it
+            bound = ((h + K * 2.0 ** -23) * ymag + h * np.abs(y) + TINY[torch.float16]) @ np.abs(dYd[t])
+            assert abs(dw[t, j] - y @ dYd[t]) <= bound + N * 2.0 ** -24 * (np.abs(ys[sl[t, j]]) @ np.abs(dYd[t]))
+        assert (np.abs(dX[t] - ref) <= 2 * h * (1 + h) * mag + h * np.abs(ref) + (k + 1) * (2.0 ** -23 * mag + TINY[torch.float16])).all()

@@ -164,3 +164,13 @@ def test_results_repeat_and_hold_in_a_captured_graph():
         # Y = (sum of weights) X, row by row
         ref = w.double().sum(1, keepdim=True) * X.double()
         assert (Y.double() - ref).abs().max() <= 2.0 ** -10 * ref.abs().max()
+
+
+@pytest.mark.parametrize("T,k,E,kind", [(40000, 8, 1024, "any"), (33000, 9, 1023, "drop"), (300000, 1, 1024, "one")])
+def test_maps_of_many_ids(T, k, E, kind):
+    """A hundred and more histograms of 1024 bins, added up by every CTA."""
+    ids = _ids(T, k, E, T, kind)
+    want_off, want_rows, want_slots = routed.sort(ids.numpy(), E)
+    offsets, rows, slots, _ = native.w4a16_moe_sort(ids.cuda(), E)
+    assert np.array_equal(offsets.cpu().numpy(), want_off) and np.array_equal(slots.cpu().numpy(), want_slots)
+    assert np.array_equal(rows.cpu().numpy()[:len(want_rows)], want_rows)
