@@ -468,3 +468,19 @@ def test_force_kernel_environment_reaches_the_routed_layers(L):
     r = _in_child({"W4A16_FORCE_KERNEL": "gemv", "W4A16_LOG": "1", "CUDA_VISIBLE_DEVICES": ""},
                   _ROUTED_CALLS.replace("moe(400, 8)", "moe(60, 8)"))
     assert "R=60 E=8 N=4096 K=4096 g=128 sym=0 -> gemv" in r.stderr
+
+
+def test_the_experts_kernel_follows_its_measurements(L):
+    """Where the decode kernel and the tensor cores were timed against each other, AUTO takes the faster:
+    (R, E, K, N, group) -> kernel."""
+    points = [(8, 16, 1024, 768, 128, "gemv"), (16, 16, 1024, 768, 128, "tc"), (16, 32, 768, 768, 128, "tc"),
+              (24, 64, 1024, 384, 128, "gemv"), (32, 64, 1024, 384, 128, "tc"), (8, 8, 1024, 1024, 128, "gemv"),
+              (12, 8, 1024, 1024, 32, "tc"), (8, 8, 2048, 2048, 128, "gemv"), (4, 4, 768, 1280, 128, "gemv"),
+              (6, 4, 768, 1280, 128, "tc"), (256, 64, 2048, 1408, 128, "gemv"), (256, 64, 2048, 1408, 32, "tc"),
+              (32, 8, 4096, 4096, 128, "gemv"), (24, 8, 4096, 4096, 32, "gemv"), (2, 8, 4096, 14336, 128, "gemv")]
+    code = _ROUTED_CALLS.split("moe = ")[0] + "; ".join(
+        f"L.w4a16_moe_gemm(p, 1, {R}, {K}, p, {E}, p, {N}, {g}, 0, p, p, 1 << 40, 0, None, None)" for R, E, K, N, g, _ in points)
+    r = _in_child({"W4A16_LOG": "1", "CUDA_VISIBLE_DEVICES": ""}, code)
+    assert r.returncode == 0, r.stderr
+    taken = [x.rsplit(" -> ")[1] for x in r.stderr.splitlines() if x.startswith("[w4a16] moe gemm")]
+    assert taken == [k for *_, k in points]

@@ -30,17 +30,21 @@ int moe_block_rows(int R, int E) {
 // bounds the mean rows of an expert that it accepts.
 int moe_gemv_max_rows(int E) { return 8 * E; }
 
-// Few rows per expert: the decode kernel. Measured, us, decode against tensor cores, by the mean rows of an expert.
+// Few rows per expert: the decode kernel. Measured with even routing and weights that come from HBM, us, decode against
+// tensor cores, by the mean rows of an expert.
 // Experts whose weights keep every SM busy: 64 of 2048 x 1408, group 128 (bf16) 21.3 / 25.9 at 0.5, 39.6 / 46.6 at 2,
 // 45.3 / 49.6 at 4, 50.5 / 51.0 at 6; group 32 (fp16), where every weight takes a scale multiply in both, 21.0 / 22.5
 // at 0.5, 42.6 / 42.9 at 3, 44.6 / 44.2 at 4; 8 of 4096 x 4096 34.0 / 38.4 at 4 (group 128), 32.6 / 35.9 at 3 (32).
-// Below 32 unit records per SM (all experts') the tensor cores' whole tiles end sooner: 16 of 1024 x 768 9.2 / 9.9 at
-// 0.5, 11.7 / 10.0 at 1, 13.3 / 10.1 at 2; 64 of 1024 x 384 11.4 / 10.3 at 0.5, 13.3 / 10.4 at 1; 8 of 2048 x 2048
-// 13.0 / 14.3 at 1, 15.9 / 14.3 at 2; 8 of 1024 x 1024 10.0 / 9.7 at 1; 4 of 768 x 1280 9.0 / 8.5 at 1, 10.3 / 8.5 at 2.
+// Below 32 unit records per SM (all experts') the tensor cores' whole tiles end sooner from about 3/8 on, where there
+// are more than 8 rows: 16 of 1024 x 768 9.3 / 10.0 at 0.5, 10.9 / 10.4 at 1; 32 of 768 x 768 9.2 / 9.2 at 0.38,
+// 10.0 / 9.3 at 0.5; 64 of 1024 x 384 10.5 / 10.5 at 0.38, 11.2 / 10.7 at 0.5; 8 of 1024 x 1024 9.8 / 10.0 at 1, 10.5 /
+// 10.1 at 1.5; 8 of 2048 x 2048 13.8 / 14.8 at 1; 4 of 768 x 1280 8.3 / 8.7 at 1, 9.2 / 8.7 at 1.5.
+// (Not every size follows: 16 of 2048 x 1408, 19 records per SM, would gain from the decode kernel up to 4, 15.3 / 19.0
+// at 1. And the host knows R alone: padded choices count, an expert with most of the rows is not seen.)
 bool moe_few_rows(int R, int E, int N, int K, int group) {
     int n_sm = gemv_stream_sm_count();
     if (n_sm <= 0) n_sm = 148;
-    if ((long long)E * (N / 128) * (K / 128) < 32ll * n_sm) return R <= (E < 8 ? E : 8) || R <= E / 2;
+    if ((long long)E * (N / 128) * (K / 128) < 32ll * n_sm) return R <= (E < 8 ? E : 8) || 8ll * R <= 3ll * E;
     return R <= 8 || (long long)R <= (group == 128 ? 4ll * E : 3ll * E);
 }
 
