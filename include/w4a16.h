@@ -389,7 +389,8 @@ W4A16_API int w4a16_gemm_noalloc(const void* A, int a_dtype, int M, int K, const
  *   workspace, ws_bytes   device, at least w4a16_moe_sort_workspace_bytes(T, k, E) bytes, 16-byte
  *              aligned (NULL when that is 0); contents on entry do not matter. Calls that share
  *              one must be ordered on the GPU.
- *   stream     cudaStream_t. One kernel launch, two above 8192 ids.
+ *   stream     cudaStream_t. One kernel launch, two above 8192 ids. Made for batches of up to some 10^5 ids:
+ *              above, the time of the maps grows with T k E (8388608 ids of 1024 experts 1.8 ms).
  *
  * w4a16_moe_sort_grad -- the gather's gradient: dX[t] = sum_j dXs[slots[t, j]], FP32 sums in the order
  *   of j, rounded once; choices without a row add nothing (a token without any gets 0).

@@ -5,7 +5,9 @@
 // (a stable counting sort), offsets[e] = #{i : e_i < e}; an id outside [0, E) has no row (slot -1).
 //   combine:  Y[t] = sum_j w[t, j] Ys[slot[t, j]]   (FP32 sums in the order of j, rounded once)
 //   gradient: dYs[slot] = w dY[t],  dw[t, j] = <dY[t], Ys[slot]>,  dX[t] = sum_j dXs[slot[t, j]]
-// All of it is bound by memory: the rows move once in and once out; everything else is small.
+// With rows to move, all of it is bound by memory: they go once in and once out. The maps are small beside them up to
+// some 10^5 ids; beyond, the histograms set the time, blocks x E counts that every CTA adds up by itself (maps alone, us:
+// 131072 ids 20.4 at 128 bins, 31.4 at 1024; 1048576 ids 91.8 and 166; 8388608 ids at 1024 bins 1790).
 #include "pdl.cuh"
 #include "routed.cuh"
 
